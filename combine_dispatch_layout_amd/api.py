@@ -17,6 +17,14 @@ masked_m, and combine with the top-k weights):
     q, scales = dispatch_fp8(x, lay)             # [R, H] e4m3fn + [R, H/128] f32
     buf, masked_m, ll_map = dispatch_ll(x, lay, cap)   # [L, cap, H]
     out = combine(expert_out, lay.src2dst, topk_weights)  # [T, H] bf16
+
+and the local experts in MXFP4, or the whole layer for a few tokens:
+
+    lay, q, s = permute_mxfp4(x, topk_ids, expert_begin, num_local_experts)
+    h, hs = grouped_swiglu_mxfp4(q, s, w13_q, w13_s, lay.counts, lay.seg_indptr)
+    y = grouped_mxfp4(h, hs, w2_q, w2_s, lay.counts, lay.seg_indptr)   # [rows, H] bf16
+    out = combine(y, lay.src2dst, topk_weights)
+    out = moe_layer(x, topk_ids, topk_weights, w13, w2, expert_begin)  # few tokens
 """
 from __future__ import annotations
 
@@ -41,6 +49,8 @@ FP8_GROUP = 128
 FP8_SCALE_UE8M0 = 1
 FP8_SCALE_COLMAJOR = 2
 FP8_SCALE_PACKED = 4
+MXFP4_GROUP = 32
+MOE_LAYER_MAX_TOKENS = 128
 
 _lib = None
 
@@ -112,6 +122,30 @@ def library():
         L.cdl_combine.restype = ctypes.c_int
         L.cdl_combine_timed.argtypes = [vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp]
         L.cdl_combine_timed.restype = ctypes.c_int
+        L.cdl_quant_mxfp4.argtypes = [vp, i64, i64, vp, vp, vp]
+        L.cdl_quant_mxfp4.restype = ctypes.c_int
+        L.cdl_dequant_mxfp4.argtypes = [vp, vp, i64, i64, vp, vp]
+        L.cdl_dequant_mxfp4.restype = ctypes.c_int
+        L.cdl_dispatch_mxfp4.argtypes = [vp, i64, i64, i32, vp, vp, vp, i64, vp, vp]
+        L.cdl_dispatch_mxfp4.restype = ctypes.c_int
+        L.cdl_permute_mxfp4.argtypes = [vp, i64, i64, i32, vp, i32, i32, i32, vp, vp, vp, vp, i64,
+                                        vp, vp, i64, vp, vp, sz, vp]
+        L.cdl_permute_mxfp4.restype = ctypes.c_int
+        L.cdl_permute_ll_mxfp4.argtypes = [vp, i64, i64, i32, vp, i32, i32, vp, vp, vp, vp, i64,
+                                           i64, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cdl_permute_ll_mxfp4.restype = ctypes.c_int
+        grouped = [vp, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64]
+        L.cdl_grouped_mxfp4.argtypes = grouped + [vp, vp, vp]
+        L.cdl_grouped_mxfp4.restype = ctypes.c_int
+        L.cdl_grouped_swiglu_mxfp4.argtypes = grouped + [vp, vp, vp, vp]
+        L.cdl_grouped_swiglu_mxfp4.restype = ctypes.c_int
+        L.cdl_moe_layer_workspace_size.argtypes = [i64, i32, i64, i32]
+        L.cdl_moe_layer_workspace_size.restype = sz
+        layer = [vp, i64, i64, i32, vp, vp, i32, i32, i64]
+        L.cdl_moe_layer.argtypes = layer + [vp, vp, vp, vp, sz, vp]
+        L.cdl_moe_layer.restype = ctypes.c_int
+        L.cdl_moe_layer_mxfp4.argtypes = layer + [vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cdl_moe_layer_mxfp4.restype = ctypes.c_int
         L.cdl_ll_expected_m.argtypes = [i64, i32, i32, i32]
         L.cdl_ll_expected_m.restype = i64
         L.cdl_status_string.argtypes = [ctypes.c_int]
@@ -691,3 +725,292 @@ def combine(y: torch.Tensor, map_: torch.Tensor, topk_weights: torch.Tensor,
 
 def ll_expected_m(T: int, num_ranks: int, k: int, num_experts: int) -> int:
     return int(library().cdl_ll_expected_m(T, num_ranks, k, num_experts))
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 rows, the grouped product, and the layer of a few tokens
+# ---------------------------------------------------------------------------
+
+def _mx_width(H: int, what: str) -> None:
+    if H < 1 or H % MXFP4_GROUP:
+        raise CdlError(-3, "%s (row length must be a multiple of %d)" % (what, MXFP4_GROUP))
+
+
+def _mx_out(out_q: Optional[torch.Tensor], out_scales: Optional[torch.Tensor], lead, H: int, device):
+    """The two buffers of [*lead, H] MXFP4 rows: given ones checked, missing
+    ones allocated."""
+    if out_q is None:
+        out_q = torch.empty(*lead, H // 2, dtype=torch.uint8, device=device)
+    if out_scales is None:
+        out_scales = torch.empty(*lead, H // MXFP4_GROUP, dtype=torch.uint8, device=device)
+    _need(out_q, "out_q", torch.uint8, (*lead, H // 2))
+    _need(out_scales, "out_scales", torch.uint8, (*lead, H // MXFP4_GROUP))
+    return out_q, out_scales
+
+
+def _mx_rows(q: torch.Tensor, scales: torch.Tensor, name: str) -> int:
+    """Row length of MXFP4 rows q [..., H / 2] with scales [..., H / 32]."""
+    _need(q, name, torch.uint8)
+    if q.dim() < 1:
+        raise ValueError("%s must have rows" % name)
+    H = 2 * q.shape[-1]
+    _mx_width(H, name)
+    _need(scales, name + " scales", torch.uint8, (*q.shape[:-1], H // MXFP4_GROUP))
+    return H
+
+
+def quant_mxfp4(x: torch.Tensor, out_q: Optional[torch.Tensor] = None,
+                out_scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of x [..., H] bf16 to MXFP4: (q [..., H / 2], scales [..., H / 32]),
+    uint8.  Groups of 32 share the smallest power-of-two scale that keeps
+    their largest magnitude within 6."""
+    _need(x, "x", torch.bfloat16)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., H]")
+    H = x.shape[-1]
+    _mx_width(H, "quant_mxfp4")
+    out_q, out_scales = _mx_out(out_q, out_scales, x.shape[:-1], H, x.device)
+    _same_device(x.device, out_q=out_q, out_scales=out_scales)
+    rc = library().cdl_quant_mxfp4(_ptr(x), x.numel() // H, H, _ptr(out_q), _ptr(out_scales), _stream(x.device))
+    _check(rc, "cdl_quant_mxfp4")
+    return out_q, out_scales
+
+
+def dequant_mxfp4(q: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """MXFP4 rows q [..., H / 2], scales [..., H / 32] as bf16 [..., H] (exact)."""
+    H = _mx_rows(q, scales, "q")
+    if out is None:
+        out = torch.empty(*q.shape[:-1], H, dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, (*q.shape[:-1], H))
+    _same_device(q.device, scales=scales, out=out)
+    rc = library().cdl_dequant_mxfp4(_ptr(q), _ptr(scales), out.numel() // H, H, _ptr(out), _stream(q.device))
+    _check(rc, "cdl_dequant_mxfp4")
+    return out
+
+
+def _mx_tokens(x: torch.Tensor, T: int) -> int:
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 2 or x.shape[0] != T:
+        raise ValueError("x must be [T, H] with T = %d" % T)
+    _mx_width(x.shape[1], "x")
+    return x.shape[1]
+
+
+def _mx_lead(out_q: Optional[torch.Tensor], out_scales: Optional[torch.Tensor], rows) -> int:
+    """Destination rows of a normal-mode scatter: a given buffer's, else `rows`."""
+    for name, t in (("out_q", out_q), ("out_scales", out_scales)):
+        if t is not None:
+            if t.dim() != 2:
+                raise ValueError("%s must be [rows, bytes]" % name)
+            return t.shape[0]
+    return int(rows)
+
+
+def dispatch_mxfp4(x: torch.Tensor, layout: Layout, out_q: Optional[torch.Tensor] = None,
+                   out_scales: Optional[torch.Tensor] = None, rows: Optional[int] = None,
+                   status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Normal-mode scatter with the rows quantised to MXFP4.  Returns
+    (q [rows, H / 2], scales [rows, H / 32])."""
+    T, k = layout.T, layout.k
+    H = _mx_tokens(x, T)
+    if out_q is None and out_scales is None and rows is None:
+        rows = layout.num_rows()
+    out_q, out_scales = _mx_out(out_q, out_scales, (_mx_lead(out_q, out_scales, rows),), H, x.device)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(x.device, src2dst=layout.src2dst, out_q=out_q, out_scales=out_scales, status=status)
+    rc = library().cdl_dispatch_mxfp4(_ptr(x), T, H, k, _ptr(layout.src2dst), _ptr(out_q), _ptr(out_scales),
+                                      out_q.shape[0], _ptr(status), _stream(x.device))
+    _check(rc, "cdl_dispatch_mxfp4")
+    return out_q, out_scales
+
+
+def permute_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, expert_begin: int, num_local_experts: int,
+                  rows: Optional[int] = None, out_q: Optional[torch.Tensor] = None,
+                  out_scales: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, alignment: int = 1):
+    """Layout + MXFP4 scatter in one call.  Returns (layout, q [rows, H / 2],
+    scales [rows, H / 32]); `rows` defaults to the upper bound of permute."""
+    lay, ws = _new_layout(topk_ids, expert_begin, num_local_experts, workspace, alignment)
+    T, k, L = lay.T, lay.k, lay.num_local_experts
+    H = _mx_tokens(x, T)
+    n = _mx_lead(out_q, out_scales, lay.reorder_buf.numel() if rows is None else rows)
+    out_q, out_scales = _mx_out(out_q, out_scales, (n,), H, x.device)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(x.device, topk_ids=lay.topk_ids, out_q=out_q, out_scales=out_scales, status=status,
+                 workspace=ws)
+    rc = library().cdl_permute_mxfp4(_ptr(x), T, H, k, _ptr(lay.topk_ids), lay.expert_begin, L, lay.alignment,
+                                     _ptr(lay.counts), _ptr(lay.seg_indptr), _ptr(lay.src2dst),
+                                     _ptr(lay.reorder_buf), lay.reorder_buf.numel(), _ptr(out_q),
+                                     _ptr(out_scales), out_q.shape[0], _ptr(status), _ptr(ws),
+                                     ws.numel() * ws.element_size(), _stream(x.device))
+    _check(rc, "cdl_permute_mxfp4")
+    return lay, out_q, out_scales
+
+
+def permute_ll_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, expert_begin: int, num_local_experts: int,
+                     cap: int, out_q: Optional[torch.Tensor] = None,
+                     out_scales: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """permute_ll with MXFP4 rows.  Returns (layout, q [L, cap, H / 2], scales
+    [L, cap, H / 32], masked_m, ll_src2dst)."""
+    lay, ws = _new_layout(topk_ids, expert_begin, num_local_experts, workspace, 1)
+    T, k, L = lay.T, lay.k, lay.num_local_experts
+    H = _mx_tokens(x, T)
+    out_q, out_scales = _mx_out(out_q, out_scales, (L, int(cap)), H, x.device)
+    masked_m = torch.empty(L, dtype=torch.int32, device=x.device)
+    ll_map = torch.empty(T * k, dtype=torch.int32, device=x.device)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(x.device, topk_ids=lay.topk_ids, out_q=out_q, out_scales=out_scales, status=status,
+                 workspace=ws)
+    rc = library().cdl_permute_ll_mxfp4(_ptr(x), T, H, k, _ptr(lay.topk_ids), lay.expert_begin, L,
+                                        _ptr(lay.counts), _ptr(lay.seg_indptr), _ptr(lay.src2dst),
+                                        _ptr(lay.reorder_buf), lay.reorder_buf.numel(), int(cap), _ptr(out_q),
+                                        _ptr(out_scales), _ptr(masked_m), _ptr(ll_map), _ptr(status), _ptr(ws),
+                                        ws.numel() * ws.element_size(), _stream(x.device))
+    _check(rc, "cdl_permute_ll_mxfp4")
+    return lay, out_q, out_scales, masked_m, ll_map
+
+
+def _grouped_args(q, scales, w_q, w_scales, counts, seg_indptr, status):
+    """Checked operands of the grouped products: (rows shape, K, L, weight
+    rows, cap)."""
+    K = _mx_rows(q, scales, "q")
+    if _mx_rows(w_q, w_scales, "w_q") != K or w_q.dim() != 3:
+        raise ValueError("w_q must be [L, N, K / 2] with K = %d, got %s" % (K, tuple(w_q.shape)))
+    L, N = w_q.shape[:2]
+    _need(counts, "counts", torch.int32, (L,))
+    if seg_indptr is not None:
+        _need(seg_indptr, "seg_indptr", torch.int64, (L + 1,))
+        if q.dim() != 2:
+            raise ValueError("q must be [rows, K / 2] with seg_indptr, got %s" % (tuple(q.shape),))
+        cap = 0
+    else:
+        if q.dim() != 3 or q.shape[0] != L:
+            raise ValueError("q must be [L, cap, K / 2] without seg_indptr, got %s" % (tuple(q.shape),))
+        cap = q.shape[1]
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(q.device, scales=scales, w_q=w_q, w_scales=w_scales, counts=counts, seg_indptr=seg_indptr,
+                 status=status)
+    return q.shape[:-1], K, L, N, cap
+
+
+def grouped_mxfp4(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor,
+                  counts: torch.Tensor, seg_indptr: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each row times its expert's weights, both MXFP4, in bf16 with fp32
+    accumulation.  w_q [L, N, K / 2].  With seg_indptr, q is [rows, K / 2] and
+    expert e owns the counts[e] rows from seg_indptr[e]; without, q is the
+    padded [L, cap, K / 2] buffer and counts its masked_m.  Rows of no expert
+    are left as they were.  Returns out [rows, N] or [L, cap, N]."""
+    lead, K, L, N, cap = _grouped_args(q, scales, w_q, w_scales, counts, seg_indptr, status)
+    if out is None:
+        out = torch.empty(*lead, N, dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, (*lead, N))
+    _same_device(q.device, out=out)
+    rc = library().cdl_grouped_mxfp4(_ptr(q), _ptr(scales), lead.numel(), K, _ptr(w_q), _ptr(w_scales), L, N,
+                                     _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status),
+                                     _stream(q.device))
+    _check(rc, "cdl_grouped_mxfp4")
+    return out
+
+
+def grouped_swiglu_mxfp4(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor,
+                         counts: torch.Tensor, seg_indptr: Optional[torch.Tensor] = None,
+                         out_q: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gate/up product with SwiGLU, quantised again in its epilogue: w_q
+    [L, 2 I, K / 2] holds the I gate rows, then the I up rows.  Returns (q
+    [rows, I / 2], scales [rows, I / 32]), the operand of the down product;
+    rows and counts as for grouped_mxfp4."""
+    lead, K, L, N, cap = _grouped_args(q, scales, w_q, w_scales, counts, seg_indptr, status)
+    if N % 2:
+        raise ValueError("w_q must hold as many gate as up rows, got %d rows" % N)
+    I = N // 2
+    _mx_width(I, "grouped_swiglu_mxfp4")
+    out_q, out_scales = _mx_out(out_q, out_scales, lead, I, q.device)
+    _same_device(q.device, out_q=out_q, out_scales=out_scales)
+    rc = library().cdl_grouped_swiglu_mxfp4(_ptr(q), _ptr(scales), lead.numel(), K, _ptr(w_q), _ptr(w_scales), L,
+                                            I, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out_q),
+                                            _ptr(out_scales), _ptr(status), _stream(q.device))
+    _check(rc, "cdl_grouped_swiglu_mxfp4")
+    return out_q, out_scales
+
+
+def moe_layer_workspace_size(T: int, k: int, I: int, L: int) -> int:
+    n = library().cdl_moe_layer_workspace_size(T, k, I, L)
+    if n == 0:
+        raise CdlError(-3, "cdl_moe_layer_workspace_size (at most %d tokens)" % MOE_LAYER_MAX_TOKENS)
+    return int(n)
+
+
+def _layer_args(x, topk_ids, topk_weights, I, L, out, workspace):
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _need_gpu(topk_ids, "topk_ids")
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError("topk_ids must be [T, k] with T = %d" % T)
+    k = topk_ids.shape[1]
+    ids = topk_ids.to(torch.int32).contiguous()
+    _need(topk_weights, "topk_weights", torch.float32, (T, k))
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    _need(out, "out", torch.bfloat16, (T, H))
+    need = moe_layer_workspace_size(T, k, I, L)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _need_gpu(workspace, "workspace")
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace too small: need %d bytes" % need)
+    _same_device(x.device, topk_ids=ids, topk_weights=topk_weights, out=out, workspace=workspace)
+    return T, H, k, ids, out, workspace
+
+
+def moe_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
+              w2: torch.Tensor, expert_begin: int = 0, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The local experts of a few tokens (T <= 128, T * k <= 4096) in two
+    kernels: out[t] = sum over local slots of w[t, j] * W2[e] h, h =
+    silu(gate) * up from w13 [L, 2 I, H] bf16 (gate rows, then up rows), w2
+    [L, H, I] bf16."""
+    _need(w13, "w13", torch.bfloat16)
+    _need(w2, "w2", torch.bfloat16)
+    if w13.dim() != 3 or w13.shape[1] % 2:
+        raise ValueError("w13 must be [L, 2 I, H], got %s" % (tuple(w13.shape),))
+    L, I = w13.shape[0], w13.shape[1] // 2
+    T, H, k, ids, out, ws = _layer_args(x, topk_ids, topk_weights, I, L, out, workspace)
+    if tuple(w13.shape) != (L, 2 * I, H) or tuple(w2.shape) != (L, H, I):
+        raise ValueError("w13 must be [L, 2 I, H] and w2 [L, H, I] with H = %d, got %s and %s"
+                         % (H, tuple(w13.shape), tuple(w2.shape)))
+    _same_device(x.device, w13=w13, w2=w2)
+    rc = library().cdl_moe_layer(_ptr(x), T, H, k, _ptr(ids), _ptr(topk_weights), int(expert_begin), L, I,
+                                 _ptr(w13), _ptr(w2), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
+                                 _stream(x.device))
+    _check(rc, "cdl_moe_layer")
+    return out
+
+
+def moe_layer_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w13_q: torch.Tensor,
+                    w13_scales: torch.Tensor, w2_q: torch.Tensor, w2_scales: torch.Tensor, expert_begin: int = 0,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_layer with MXFP4 weights (w13_q [L, 2 I, H / 2], w2_q [L, H, I / 2]
+    and their scales); the activations stay bf16."""
+    H13, I2 = _mx_rows(w13_q, w13_scales, "w13_q"), _mx_rows(w2_q, w2_scales, "w2_q")
+    if w13_q.dim() != 3 or w13_q.shape[1] != 2 * I2:
+        raise ValueError("w13_q must be [L, 2 I, H / 2] with I = %d, got %s" % (I2, tuple(w13_q.shape)))
+    L, I = w13_q.shape[0], I2
+    T, H, k, ids, out, ws = _layer_args(x, topk_ids, topk_weights, I, L, out, workspace)
+    if H13 != H or tuple(w2_q.shape) != (L, H, I // 2):
+        raise ValueError("w13_q and w2_q must be [L, 2 I, H / 2] and [L, H, I / 2] with H = %d, got %s and %s"
+                         % (H, tuple(w13_q.shape), tuple(w2_q.shape)))
+    _same_device(x.device, w13_q=w13_q, w13_scales=w13_scales, w2_q=w2_q, w2_scales=w2_scales)
+    rc = library().cdl_moe_layer_mxfp4(_ptr(x), T, H, k, _ptr(ids), _ptr(topk_weights), int(expert_begin), L, I,
+                                       _ptr(w13_q), _ptr(w13_scales), _ptr(w2_q), _ptr(w2_scales), _ptr(out),
+                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(x.device))
+    _check(rc, "cdl_moe_layer_mxfp4")
+    return out

@@ -17,7 +17,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
-SOURCES = [os.path.join(PKG, "csrc", "cdl.hip")]
+SOURCES = [os.path.join(PKG, "csrc", "libcdl.hip")]
 LIB = os.path.join(PKG, "libcdl.so")
 ARCH = "gfx950"
 

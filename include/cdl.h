@@ -10,7 +10,8 @@
  *
  *   layout  (routing histogram, prefix sum, stable slot ranks)
  *     -> dispatch (row scatter: normal / low-latency padded / fp8 groups)
- *     -> [expert computation, outside this library]
+ *     -> [expert computation: outside this library, or the grouped MXFP4
+ *         product below]
  *     -> combine (gather + top-k-weighted sum per token, fp32 accumulation)
  *
  * Conventions shared by every entry point:
@@ -77,6 +78,8 @@ extern "C" {
                                        with 32-bit byte offsets); larger H is CDL_ERR_TOO_LARGE */
 #define CDL_MAX_LOCAL_EXPERTS 2048
 #define CDL_FP8_GROUP 128
+#define CDL_MXFP4_GROUP 32
+#define CDL_MOE_LAYER_MAX_TOKENS 128
 
 /* fp8 scale formats (bit flags) -- see cdl_dispatch_fp8_ex */
 #define CDL_FP8_SCALE_UE8M0 1       /* power-of-two scales */
@@ -472,6 +475,156 @@ int cdl_combine(const uint16_t *y, int64_t y_rows, int64_t H, const int32_t *map
 int cdl_combine_timed(const uint16_t *y, int64_t y_rows, int64_t H, const int32_t *map,
                       const float *topk_weights, int64_t T, int32_t k, uint16_t *out,
                       int32_t *status, void *start_event, void *stop_event, void *stream);
+
+/*
+ * MXFP4 rows (OCP microscaling, e2m1 elements): every group of
+ * CDL_MXFP4_GROUP consecutive elements of a row shares a scale 2^e, stored as
+ * the byte e + 127 (E8M0); an element is 4 bits (sign, two exponent bits, one
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 times the scale), two to a byte,
+ * the even element in the low half.  A row of H elements is H / 2 bytes and
+ * H / 32 scale bytes, both row-major.
+ *
+ * Quantisation of a group: e is the smallest integer >= -127 with
+ * 6 * 2^e >= amax (nothing saturates), each code the one nearest to x / 2^e,
+ * ties to the even code, the sign kept (of zeros too); a zero group has e =
+ * -127.  Non-finite values: a group with an infinity takes e = 127, so that
+ * it reads back as infinity (its finite elements keep what 2^127 leaves of
+ * them); a group with a NaN takes the scale's NaN code (255) with all codes
+ * zero and reads back as NaN.
+ *
+ * Every MXFP4 call needs a row length that is a multiple of 32
+ * (CDL_ERR_UNSUPPORTED otherwise), at most CDL_MAX_HIDDEN.
+ */
+
+/*
+ * cdl_quant_mxfp4 -- rows to MXFP4 (weights once at load, or activations
+ * outside a scatter).
+ *   x       in  [rows, H] bf16, 16-byte aligned
+ *   q       out [rows, H / 2] bytes, 8-byte aligned
+ *   scales  out [rows, H / 32] bytes
+ */
+int cdl_quant_mxfp4(const uint16_t *x, int64_t rows, int64_t H, uint8_t *q, uint8_t *scales,
+                    void *stream);
+
+/*
+ * cdl_dequant_mxfp4 -- MXFP4 rows back to bf16 (exact; magnitudes from 2^128
+ * on are infinite).  q 8-byte, out 16-byte aligned.
+ */
+int cdl_dequant_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t H,
+                      uint16_t *out, void *stream);
+
+/*
+ * cdl_dispatch_mxfp4 -- cdl_dispatch with every row quantised to MXFP4 on
+ * the scatter.  out_q [cap_rows, H / 2] (8-byte aligned), out_scales
+ * [cap_rows, H / 32]; x 16-byte aligned; the rest as for cdl_dispatch.
+ */
+int cdl_dispatch_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *src2dst,
+                       uint8_t *out_q, uint8_t *out_scales, int64_t cap_rows, int32_t *status,
+                       void *stream);
+
+/*
+ * cdl_permute_mxfp4 -- cdl_permute with MXFP4 rows: the layout, then the
+ * scatter of cdl_dispatch_mxfp4.
+ */
+int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,
+                      int32_t expert_begin, int32_t L, int32_t alignment, int32_t *counts,
+                      int64_t *seg_indptr, int32_t *src2dst, int32_t *reorder_topk_ids,
+                      int64_t reorder_cap, uint8_t *out_q, uint8_t *out_scales, int64_t cap_rows,
+                      int32_t *status, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * cdl_permute_ll_mxfp4 -- cdl_permute_ll with MXFP4 rows: out_q
+ * [L, cap, H / 2], out_scales [L, cap, H / 32].
+ */
+int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
+                         const int32_t *topk_ids, int32_t expert_begin, int32_t L, int32_t *counts,
+                         int64_t *seg_indptr, int32_t *src2dst, int32_t *reorder_topk_ids,
+                         int64_t reorder_cap, int64_t cap, uint8_t *out_q, uint8_t *out_scales,
+                         int32_t *masked_m, int32_t *ll_src2dst, int32_t *status, void *ws,
+                         size_t ws_bytes, void *stream);
+
+/*
+ * cdl_grouped_mxfp4 -- each dispatched row times its expert's weights, both
+ * MXFP4: out[r, n] = bf16_rne(sum_k a[r, k] * w[e, n, k]), e the row's
+ * expert, accumulated in fp32.
+ *
+ *   q, scales      in  [rows, K / 2] and [rows, K / 32] bytes
+ *   w_q, w_scales  in  [L, N, K / 2] and [L, N, K / 32] bytes
+ *   counts         in  [L] int32 rows of every expert
+ *   seg_indptr     in  [L + 1] int64 first row of every expert (normal mode;
+ *                      segments may be padded), or NULL: the rows of expert e
+ *                      start at e * cap (low latency: counts is masked_m, and
+ *                      rows == L * cap)
+ *   out            out [rows, N] bf16; only the counts[e] rows of every
+ *                      expert are written
+ *   status         out device int32 (may be NULL): a count that does not fit
+ *                      the buffer is cut to what does and sets
+ *                      CDL_STATUS_ROWS_OVERFLOW (segments) or
+ *                      CDL_STATUS_LL_OVERFLOW (padded)
+ * K % 32 == 0, q and w_q 16-byte aligned; any N >= 1.
+ */
+int cdl_grouped_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t K,
+                      const uint8_t *w_q, const uint8_t *w_scales, int32_t L, int64_t N,
+                      const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *out,
+                      int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_swiglu_mxfp4 -- the gate/up product with SwiGLU and
+ * quantisation in its epilogue: with w [L, 2 I, K] the I gate rows followed by
+ * the I up rows of every expert, g and u the two products in fp32 and
+ * h = g / (1 + exp(-g)) * u in fp32, the rows h are written as MXFP4:
+ * out_q [rows, I / 2] (16-byte aligned), out_scales [rows, I / 32], the
+ * input of the down product.  I % 32 == 0; the rest as cdl_grouped_mxfp4.
+ */
+int cdl_grouped_swiglu_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t K,
+                             const uint8_t *w_q, const uint8_t *w_scales, int32_t L, int64_t I,
+                             const int32_t *counts, const int64_t *seg_indptr, int64_t cap,
+                             uint8_t *out_q, uint8_t *out_scales, int32_t *status, void *stream);
+
+/*
+ * cdl_moe_layer_workspace_size -- device workspace bytes of cdl_moe_layer and
+ * cdl_moe_layer_mxfp4 (routing lists and the activations between the two
+ * products); 0 for sizes they reject.
+ */
+size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
+
+/*
+ * cdl_moe_layer -- the local experts of a few tokens, from token rows to
+ * token rows in two kernels (no layout, scatter or combine between):
+ *
+ *   out[t] = bf16_rne(sum over valid j of w[t, j] * W2[e] bf16_rne(h)),
+ *   h = g / (1 + exp(-g)) * u,  (g, u) = W13[e] x[t],  e = e_{t, j}
+ *
+ * with fp32 accumulation; h is rounded to bf16, the operand type of the
+ * second product.  A token with no valid slot gets +0.
+ *
+ *   x             in  [T, H] bf16
+ *   topk_ids, topk_weights, expert_begin, L   as for the layout and cdl_combine
+ *   w13           in  [L, 2 I, H] bf16: the I gate rows, then the I up rows
+ *   w2            in  [L, H, I] bf16
+ *   out           out [T, H] bf16
+ *   ws, ws_bytes      cdl_moe_layer_workspace_size bytes, 16-byte aligned, no
+ *                     initialisation needed; calls that overlap need their own
+ * T <= CDL_MOE_LAYER_MAX_TOKENS and T * k <= 4096 (CDL_ERR_UNSUPPORTED
+ * otherwise: larger batches take the permute, the grouped products and the
+ * combine); H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte aligned.  The
+ * sums are taken in a fixed order: the result is deterministic.
+ */
+int cdl_moe_layer(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,
+                  const float *topk_weights, int32_t expert_begin, int32_t L, int64_t I,
+                  const uint16_t *w13, const uint16_t *w2, uint16_t *out, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/*
+ * cdl_moe_layer_mxfp4 -- cdl_moe_layer with MXFP4 weights (w13_q [L, 2 I,
+ * H / 2], w13_scales [L, 2 I, H / 32], w2_q [L, H, I / 2], w2_scales [L, H,
+ * I / 32]); the activations stay bf16.  H % 32 == 0 and I % 32 == 0.
+ */
+int cdl_moe_layer_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
+                        const int32_t *topk_ids, const float *topk_weights, int32_t expert_begin,
+                        int32_t L, int64_t I, const uint8_t *w13_q, const uint8_t *w13_scales,
+                        const uint8_t *w2_q, const uint8_t *w2_scales, uint16_t *out, void *ws,
+                        size_t ws_bytes, void *stream);
 
 /*
  * cdl_ll_expected_m -- host-side hint for the masked grouped GEMM after a
