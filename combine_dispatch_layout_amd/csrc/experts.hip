@@ -810,8 +810,7 @@ __global__ __launch_bounds__(kGroupedThreads) void grouped_kernel(GroupedArgs a,
 // ---------------------------------------------------------------------------
 
 constexpr int kFewThreads = 256;        // first kernel: 4 waves share the columns, split the depth
-constexpr int kFewWaves2 = 8;           // second kernel
-constexpr int kFewChunk = 512;          // depth of one item of the second kernel
+constexpr int kFewWaves = kFewThreads / kWave;
 constexpr int kFewMaxSlots = 4096;
 
 struct FewArgs {
@@ -827,22 +826,13 @@ struct FewArgs {
     uint16_t *h;                 // [T k, I]
 };
 
-// Routing lists in the workspace, written by the first kernel's workgroup 0:
-// the number of experts with slots, then for the a-th of them its index and
-// the begin of its slots, then the slots (flat t * k + j, ascending).
+// Routing lists in the workspace, written by the first kernel: the number of
+// experts with slots, then for the a-th of them its index and the begin of
+// its slots, then the slots (flat t * k + j, ascending within an expert).
 struct FewLists {
     int32_t *active, *expert, *begin, *slots;
     __host__ __device__ FewLists(int32_t *p, int A) : active(p), expert(p + 4), begin(p + 4 + A), slots(p + 4 + 2 * A + 4) {}
     static size_t ints(int64_t A, int64_t n) { return (size_t)(4 + A + A + 4 + n); }
-};
-
-// A 16-row operand fragment of v_mfma_f32_16x16x32_bf16 for one step: lane l
-// holds row l % 16 and 8 consecutive elements.  MXFP4 weights: a lane's 16
-// bytes are one group of 32 elements, which serve 4 steps of 8.
-template <bool FP4>
-struct FewStep {
-    static constexpr int kDepth = FP4 ? 128 : 32;         // elements of the contraction per load
-    static constexpr int kSteps = FP4 ? 4 : 1;            // matrix instructions per load
 };
 
 template <int STEP>
@@ -856,202 +846,495 @@ __device__ __forceinline__ v8bf16 few_expand(u32x4 w, float p)
     return __builtin_bit_cast(v8bf16, r);
 }
 
-// acc[i] += W_i (16 rows each) * B over the depth steps [d0, d1) with stride:
-// W_i rows and the lane's B row (bf16, 16 columns) through descriptors, which
-// return zeros past a row block's or row's end.
-//   wq[i], ws[i]  descriptors of the 16 weight rows (scales: FP4 only)
-//   br            descriptor of the lane's operand rows' common base, b_off the lane's row offset in bytes
-template <bool FP4, int NW>
-__device__ __forceinline__ void few_product(f32x4 (&acc)[NW], const rsrc_t (&wq)[NW], const rsrc_t (&ws)[NW],
-                                            const uint16_t *brow, int64_t depth, int64_t d0, int64_t d1,
-                                            int64_t stride)
-{
-    const int lane = threadIdx.x & (kWave - 1);
-    const int r = lane & 15, g = lane >> 4;
-    for (int64_t d = d0; d < d1; d += stride) {
+// 16 rows of weights through descriptors of their own (zeros past them).
+// MXFP4 scale rows start at any byte: their descriptor begins at the word
+// below (`shift` bytes before) and ends with the word that holds the last one.
+template <bool FP4>
+struct FewRows {
+    rsrc_t q, s;
+    uint32_t shift;
+    __device__ __forceinline__ FewRows() {}
+    __device__ __forceinline__ FewRows(const uint8_t *w, const uint8_t *ws, int64_t row, int64_t rows, int64_t depth)
+    {
+        if (rows < 0) rows = 0;
         if constexpr (FP4) {
-            const int64_t at = d + 32 * g;
-            const bool in = at < depth;
-            const uint32_t wo = in ? (uint32_t)(r * (depth / 2) + at / 2) : 0xFFFFFFF0u;
-            const uint32_t so = in ? (uint32_t)(r * (depth / 32) + at / 32) : 0xFFFFFFF0u;
-            u32x4 b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                b[i] = in ? *reinterpret_cast<const u32x4 *>(brow + at + 8 * i) : u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const u32x4 w = buf_ld16(wq[i], wo, 0);
-                const float p = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(ws[i], so, 0, 0) << 23);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_expand<0>(w, p), __builtin_bit_cast(v8bf16, b[0]), acc[i], 0, 0, 0);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_expand<1>(w, p), __builtin_bit_cast(v8bf16, b[1]), acc[i], 0, 0, 0);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_expand<2>(w, p), __builtin_bit_cast(v8bf16, b[2]), acc[i], 0, 0, 0);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_expand<3>(w, p), __builtin_bit_cast(v8bf16, b[3]), acc[i], 0, 0, 0);
-            }
+            q = make_rsrc(w + row * (depth / 2), (uint32_t)(rows * (depth / 2)));
+            const uint8_t *sp = ws + row * (depth / 32);
+            shift = (uint32_t)(uintptr_t)sp & 3u;
+            s = make_rsrc(sp - shift, rows ? (uint32_t)(shift + rows * (depth / 32) + 3) & ~3u : 0u);
         } else {
-            const int64_t at = d + 8 * g;
-            const bool in = at < depth;
-            const uint32_t wo = in ? (uint32_t)(r * (depth * 2) + at * 2) : 0xFFFFFFF0u;
-            const u32x4 b = in ? *reinterpret_cast<const u32x4 *>(brow + at) : u32x4{0, 0, 0, 0};
+            q = make_rsrc(w + row * depth * 2, (uint32_t)(rows * depth * 2));
+            shift = 0;
+        }
+    }
+};
+
+// The depth is taken in turns of 256 elements.  v_mfma_f32_16x16x32_bf16: lane
+// l holds row (column) l % 16 of its operand and 8 consecutive elements; the
+// order of the depth is free as long as both operands share it.  bf16: step i
+// of a turn is elements 32 i + 8 (l / 16) on, one 16-byte load per 16 rows.
+// MXFP4: a lane's 16 bytes are one group of 32 elements, which serve 4
+// instructions; step i (of 2) of a turn is group 2 (l / 16) + i, so that a
+// lane's two scale bytes are neighbours and arrive in one load.
+constexpr uint32_t kTurn = 256;
+
+// The weights of G steps of NW blocks of 16 rows.
+template <bool FP4, int NW, int G>
+struct FewWeights {
+    static_assert(!FP4 || G == 2, "a turn of MXFP4 weights is two steps");
+    u32x4 w[G][NW];
+    u32x2 s[NW];
+    uint32_t at[NW];                           // byte of the lane's first scale in its words, at % 4
+
+    // steps from `first` on of the turn at element d; past `depth` no memory is read
+    __device__ __forceinline__ void load(const FewRows<FP4> (&rows)[NW], uint32_t depth, uint32_t d, int first)
+    {
+        const uint32_t lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const u32x4 w = buf_ld16(wq[i], wo, 0);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, w), __builtin_bit_cast(v8bf16, b), acc[i], 0, 0, 0);
+        for (int j = 0; j < G; ++j) {
+            const uint32_t at = FP4 ? d + (2 * g + j) * 32 : d + (first + j) * 32 + g * 8;
+            const uint32_t off = at < depth ? (FP4 ? r * (depth / 2) + at / 2 : (r * depth + at) * 2) : 0xFFFFFFF0u;
+#pragma unroll
+            for (int n = 0; n < NW; ++n) w[j][n] = buf_ld16(rows[n].q, off, 0);
+        }
+        if constexpr (FP4) {
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                at[n] = rows[n].shift + r * (depth / 32) + d / 32 + 2 * g;
+                s[n] = __builtin_amdgcn_raw_buffer_load_b64(rows[n].s, at[n] & ~3u, 0, 0);
             }
         }
     }
-}
-
-template <bool FP4>
-__device__ __forceinline__ void few_weight_rows(const uint8_t *w, const uint8_t *s, int64_t row, int64_t rows,
-                                                int64_t depth, rsrc_t *q, rsrc_t *sc)
-{
-    if constexpr (FP4) {
-        *q = make_rsrc(w + row * (depth / 2), (uint32_t)(rows * (depth / 2)));
-        *sc = make_rsrc(s + row * (depth / 32), (uint32_t)(rows * (depth / 32)));
-    } else {
-        *q = make_rsrc(w + row * depth * 2, (uint32_t)(rows * depth * 2));
-        *sc = *q;
+    // acc[n] += block n * columns; column(chunk) is the lane's column's 8
+    // elements from 8 chunk on of the turn
+    template <typename F>
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[NW], uint32_t depth, uint32_t d, int first, F &&column)
+    {
+        const uint32_t lane = threadIdx.x & (kWave - 1), g = lane >> 4;
+        if constexpr (FP4) {
+            uint32_t bytes[NW];
+#pragma unroll
+            for (int n = 0; n < NW; ++n) bytes[n] = __builtin_amdgcn_alignbyte(s[n].y, s[n].x, at[n] & 3u);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                v8bf16 b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = column((2 * g + j) * 4 + i);
+                const bool in = d + (2 * g + j) * 32 < depth;
+                float p[NW];
+#pragma unroll
+                for (int n = 0; n < NW; ++n) {
+                    // (past the depth: codes and scale zero)
+                    p[n] = __uint_as_float(in ? (bytes[n] >> (8 * j) & 0xFFu) << 23 : 0u);
+                }
+                auto part = [&](auto c) {
+                    constexpr int st = decltype(c)::value;
+#pragma unroll
+                    for (int n = 0; n < NW; ++n)
+                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_expand<st>(w[j][n], p[n]), b[st], acc[n], 0, 0, 0);
+                };
+                part(std::integral_constant<int, 0>{});
+                part(std::integral_constant<int, 1>{});
+                part(std::integral_constant<int, 2>{});
+                part(std::integral_constant<int, 3>{});
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const v8bf16 b = column((first + j) * 4 + g);
+#pragma unroll
+                for (int n = 0; n < NW; ++n)
+                    acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, w[j][n]), b, acc[n], 0, 0, 0);
+            }
+        }
     }
-}
+};
 
-// First kernel: h[slot, i] = silu(gate) * up for 16 columns i of the a-th
-// active expert (blockIdx.y); blockIdx.x the column tile.
-template <bool FP4>
-__global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a)
+// A turn of up to 2 XT bf16 rows, the columns of the product, on its way
+// through a wave's own 16 x 512 bytes of LDS: a load brings two rows (32 lanes
+// of 16 bytes each), where fragments straight from memory would take a load
+// of 64 lanes for every 32 elements whatever the number of rows.  16-byte
+// chunk q of row r lies at q ^ r.
+constexpr int kColumnBytes = 16 * 512;
+template <int XT>
+struct FewColumns {
+    u32x4 v[XT];
+    uint8_t *lds;
+
+    // row_off(i): byte offset of row i; elements past `depth` are zero
+    template <typename F>
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t depth, uint32_t d, F &&row_off)
+    {
+        const uint32_t lane = threadIdx.x & (kWave - 1), at = d + (lane & 31) * 8;
+#pragma unroll
+        for (int j = 0; j < XT; ++j) {
+            const uint32_t off = row_off(2 * j + (int)(lane >> 5)) + at * 2;
+            v[j] = buf_ld16(r, at < depth ? off : 0xFFFFFFF0u, 0);
+        }
+    }
+    __device__ __forceinline__ void store() const
+    {
+        const uint32_t lane = threadIdx.x & (kWave - 1), q = lane & 31;
+#pragma unroll
+        for (int j = 0; j < XT; ++j) {
+            const uint32_t r = 2 * j + (lane >> 5);
+            *reinterpret_cast<u32x4 *>(lds + r * 512 + ((q ^ r) << 4)) = v[j];
+        }
+    }
+    // the lane's column (rows from 2 XT on repeat the first ones: unused columns)
+    __device__ __forceinline__ v8bf16 chunk(uint32_t q) const
+    {
+        const uint32_t r = (threadIdx.x & 15) & (2 * XT - 1);
+        return *reinterpret_cast<const v8bf16 *>(lds + r * 512 + ((q ^ r) << 4));
+    }
+};
+
+__device__ __forceinline__ uint64_t lanes_below(int lane) { return lane ? ~0ull >> (kWave - lane) : 0ull; }
+
+// First kernel: h[slot, i] = silu(gate) * up for 16 CB columns i of the a-th
+// expert with slots (blockIdx.y); blockIdx.x is the column tile.  The 4 waves
+// take the turns of the depth in rotation, a part of a turn being multiplied
+// while the next one arrives, and add their sums in LDS.
+template <bool FP4, int CB>
+__global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
 {
+    constexpr int NW = 2 * CB;
     extern __shared__ int32_t lds[];
     int32_t *hist = lds;                       // [L]
     int32_t *list = lds + a.L;                 // [n] the expert's slots
     int16_t *es = reinterpret_cast<int16_t *>(list + a.T * a.k);   // [n] local expert of each slot
-    __shared__ f32x4 part[4][2][kWave];
+    __shared__ f32x4 part[kFewWaves][NW][kWave];
+    __shared__ u32x4 columns[kFewWaves][kColumnBytes / 16];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
     const int n = a.T * a.k;
-    for (int e = tid; e < a.L; e += kFewThreads) hist[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kFewThreads) {
-        const int e = local_expert(a.ids[i], a.expert_begin, a.L);
-        es[i] = (int16_t)e;
-        if (e >= 0) atomicAdd(&hist[e], 1);
-    }
-    __syncthreads();
-    // the blockIdx.y-th expert with slots, and the slots of those before it
-    int mine = -1, seen = 0, before = 0;
-    int32_t slots_seen = 0;
-    for (int e0 = 0; e0 < a.L; e0 += kWave) {
-        const int32_t c = e0 + lane < a.L ? hist[e0 + lane] : 0;
-        const uint64_t m = __ballot(c > 0);
-        const int rank = seen + __popcll(m & (lane ? ~0ull >> (kWave - lane) : 0ull));
-        const int32_t incl = slots_seen + wave_inclusive_scan(c);
-        const uint64_t hit = __ballot(c > 0 && rank == (int)blockIdx.y);
-        if (hit) {
-            const int l = (int)__builtin_ctzll(hit);
-            mine = e0 + l;
-            before = __builtin_amdgcn_readlane(incl - c, l);
-        }
-        seen += __popcll(m);
-        slots_seen = __builtin_amdgcn_readlane(incl, kWave - 1);
-    }
-    // the routing lists of the second kernel: every expert's first workgroup
-    // writes the expert's own
     const FewLists ls(a.lists, n < a.L ? n : a.L);
     const bool publish = blockIdx.x == 0 && wave == 0;
-    if (publish && lane == 0) {
-        if (blockIdx.y == 0) ls.active[0] = seen;
-        if (mine >= 0) {
-            ls.expert[blockIdx.y] = mine;
-            ls.begin[blockIdx.y] = before;
-            ls.begin[blockIdx.y + 1] = before + hist[mine];
+    int mine = -1, count = 0, one_slot = 0;
+    if (n <= kWave) {
+        // every wave finds the expert by itself: slot i lies in lane i, the
+        // experts in the order of their first slots
+        const int e = lane < n ? local_expert(a.ids[lane], a.expert_begin, a.L) : -1;
+        uint64_t left = __ballot(e >= 0), mask = 0;
+        int a_th = 0, before = 0;
+        while (left) {
+            const int el = __builtin_amdgcn_readlane(e, (int)__builtin_ctzll(left));
+            const uint64_t m = __ballot(e == el);
+            if (a_th == (int)blockIdx.y) {
+                mine = el;
+                mask = m;
+            }
+            if (a_th < (int)blockIdx.y) before += __popcll(m);
+            ++a_th;
+            left &= ~m;
         }
-    }
-    if (mine < 0) return;
-    if (wave == 0) {
+        count = __popcll(mask);
+        if (publish) {
+            if (lane == 0) {
+                if (blockIdx.y == 0) ls.active[0] = a_th;
+                if (mine >= 0) {
+                    ls.expert[blockIdx.y] = mine;
+                    ls.begin[blockIdx.y] = before;
+                    ls.begin[blockIdx.y + 1] = before + count;
+                }
+            }
+            if (mask >> lane & 1) ls.slots[before + __popcll(mask & lanes_below(lane))] = lane;
+        }
+        if (mine < 0) return;
+        // lane i takes the expert's i-th slot
         int at = 0;
-        for (int i0 = 0; i0 < n; i0 += kWave) {
-            const bool is = i0 + lane < n && es[i0 + lane] == mine;
-            const uint64_t m = __ballot(is);
-            if (is) {
-                const int to = at + __popcll(m & (lane ? ~0ull >> (kWave - lane) : 0ull));
-                list[to] = i0 + lane;
-                if (publish) ls.slots[before + to] = i0 + lane;
-            }
-            at += __popcll(m);
+        for (uint64_t m = mask; m; m &= m - 1, ++at) {
+            const int slot = (int)__builtin_ctzll(m);
+            if (at == lane) one_slot = slot;
         }
-    }
-    const int count = hist[mine];
-    __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * 16;
-    const int64_t rows = a.I - i0 < 16 ? a.I - i0 : 16;
-    rsrc_t wq[2], ws[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        few_weight_rows<FP4>(a.w13, a.w13_s, (int64_t)mine * 2 * a.I + i * a.I + i0, rows, a.H, &wq[i], &ws[i]);
-    const int c = lane & 15, g = lane >> 4;
-    for (int c0 = 0; c0 < count; c0 += 16) {
-        const int slot = list[c0 + c < count ? c0 + c : c0];
-        const uint16_t *xrow = a.x + (int64_t)(slot / a.k) * a.H;
-        f32x4 acc[2] = {};
-        constexpr int D = FewStep<FP4>::kDepth;
-        few_product<FP4, 2>(acc, wq, ws, xrow, a.H, (int64_t)wave * D, a.H, 4 * D);
-        if (c0) __syncthreads();               // the sums of the round before are read
-        part[wave][0][lane] = acc[0];
-        part[wave][1][lane] = acc[1];
+    } else {
+        for (int e = tid; e < a.L; e += kFewThreads) hist[e] = 0;
         __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int w = 1; w < 4; ++w) {
-                acc[0] += part[w][0][lane];
-                acc[1] += part[w][1][lane];
+        for (int i = tid; i < n; i += kFewThreads) {
+            const int e = local_expert(a.ids[i], a.expert_begin, a.L);
+            es[i] = (int16_t)e;
+            if (e >= 0) atomicAdd(&hist[e], 1);
+        }
+        __syncthreads();
+        // the blockIdx.y-th expert with slots, and the slots of those before it
+        int seen = 0, before = 0;
+        int32_t slots_seen = 0;
+        for (int e0 = 0; e0 < a.L; e0 += kWave) {
+            const int32_t c = e0 + lane < a.L ? hist[e0 + lane] : 0;
+            const uint64_t m = __ballot(c > 0);
+            const int rank = seen + __popcll(m & lanes_below(lane));
+            const int32_t incl = slots_seen + wave_inclusive_scan(c);
+            const uint64_t hit = __ballot(c > 0 && rank == (int)blockIdx.y);
+            if (hit) {
+                const int l = (int)__builtin_ctzll(hit);
+                mine = e0 + l;
+                before = __builtin_amdgcn_readlane(incl - c, l);
             }
-            if (c0 + c < count) {
+            seen += __popcll(m);
+            slots_seen = __builtin_amdgcn_readlane(incl, kWave - 1);
+        }
+        // every expert's first workgroup writes the expert's own list
+        if (publish && lane == 0) {
+            if (blockIdx.y == 0) ls.active[0] = seen;
+            if (mine >= 0) {
+                ls.expert[blockIdx.y] = mine;
+                ls.begin[blockIdx.y] = before;
+                ls.begin[blockIdx.y + 1] = before + hist[mine];
+            }
+        }
+        if (mine < 0) return;
+        if (wave == 0) {
+            int at = 0;
+            for (int i0 = 0; i0 < n; i0 += kWave) {
+                const bool is = i0 + lane < n && es[i0 + lane] == mine;
+                const uint64_t m = __ballot(is);
+                if (is) {
+                    const int to = at + __popcll(m & lanes_below(lane));
+                    list[to] = i0 + lane;
+                    if (publish) ls.slots[before + to] = i0 + lane;
+                }
+                at += __popcll(m);
+            }
+        }
+        count = hist[mine];
+        __syncthreads();
+    }
+    mine = __builtin_amdgcn_readfirstlane(mine);
+    const int64_t i0 = (int64_t)blockIdx.x * 16 * CB;
+    FewRows<FP4> rows[NW];                     // gate blocks, then up blocks
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const int64_t c = i0 + i % CB * 16, left = a.I - c;
+        rows[i] = FewRows<FP4>(a.w13, a.w13_s, (int64_t)mine * 2 * a.I + i / CB * a.I + (left > 0 ? c : 0),
+                               left < 16 ? left : 16, a.H);
+    }
+    const int c = lane & 15, g = lane >> 4;
+    const uint32_t H = (uint32_t)a.H;
+    const rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.T * a.H * 2));
+    auto slot_of = [&](int i) {                // the expert's i-th slot
+        return n <= kWave ? __shfl(one_slot, i, kWave) : list[i];
+    };
+    for (int c0 = 0; c0 < count; c0 += 16) {
+        const int live = count - c0 < 16 ? count - c0 : 16;
+        const int slot = slot_of(c0 + (c < live ? c : 0));
+        f32x4 acc[NW] = {};
+        uint8_t *mine_lds = reinterpret_cast<uint8_t *>(columns[wave]);
+        auto product = [&](auto rows2) {
+            constexpr int XT = decltype(rows2)::value;
+            constexpr int G = FP4 ? 2 : 4;
+            FewColumns<XT> x;
+            x.lds = mine_lds;
+            uint32_t off[XT];
+#pragma unroll
+            for (int j = 0; j < XT; ++j) {
+                const int i = 2 * j + (lane >> 5);
+                off[j] = (uint32_t)(slot_of(c0 + (i < live ? i : 0)) / a.k) * H * 2;
+            }
+            auto load_x = [&](uint32_t d) { x.load(xr, H, d, [&](int i) { return off[i / 2]; }); };
+            auto column = [&](uint32_t q) { return x.chunk(q); };
+            FewWeights<FP4, NW, G> w[2];
+            constexpr uint32_t kNext = kTurn * kFewWaves;
+            uint32_t d = (uint32_t)wave * kTurn;
+            load_x(d);
+            w[0].load(rows, H, d, 0);
+            x.store();
+            load_x(d + kNext);
+            if constexpr (FP4) {
+                // a part is a turn
+                for (; d < H; d += 2 * kNext) {
+                    w[1].load(rows, H, d + kNext, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    w[0].multiply(acc, H, d, 0, column);
+                    x.store();
+                    load_x(d + 2 * kNext);
+                    __builtin_amdgcn_sched_barrier(0);
+                    w[0].load(rows, H, d + 2 * kNext, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    w[1].multiply(acc, H, d + kNext, 0, column);
+                    x.store();
+                    load_x(d + 3 * kNext);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+                // a part is half a turn
+                for (; d < H; d += kNext) {
+                    w[1].load(rows, H, d, 4);
+                    __builtin_amdgcn_sched_barrier(0);
+                    w[0].multiply(acc, H, d, 0, column);
+                    __builtin_amdgcn_sched_barrier(0);
+                    w[0].load(rows, H, d + kNext, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    w[1].multiply(acc, H, d, 4, column);
+                    x.store();
+                    load_x(d + 2 * kNext);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        };
+        if (live <= 2)
+            product(std::integral_constant<int, 1>{});
+        else if (live <= 4)
+            product(std::integral_constant<int, 2>{});
+        else if (live <= 8)
+            product(std::integral_constant<int, 4>{});
+        else
+            product(std::integral_constant<int, 8>{});
+        if (c0) __syncthreads();               // the sums of the round before are read
+#pragma unroll
+        for (int i = 0; i < NW; ++i) part[wave][i][lane] = acc[i];
+        __syncthreads();
+        // wave b adds column block b
+        if (wave < CB) {
+            f32x4 gate = part[0][wave][lane], up = part[0][CB + wave][lane];
+#pragma unroll
+            for (int w = 1; w < kFewWaves; ++w) {
+                gate += part[w][wave][lane];
+                up += part[w][CB + wave][lane];
+            }
+            const int64_t col0 = i0 + wave * 16 + 4 * g;
+            if (c < live && col0 < a.I) {
                 float h[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = acc[0][i] / (1.0f + __expf(-acc[0][i])) * acc[1][i];
-                if (4 * g < rows)
-                    *reinterpret_cast<u32x2 *>(a.h + (int64_t)slot * a.I + i0 + 4 * g) =
-                        u32x2{pack_bf16_rne(h[0], h[1]), pack_bf16_rne(h[2], h[3])};
+                for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i];
+                *reinterpret_cast<u32x2 *>(a.h + (int64_t)slot * a.I + col0) =
+                    u32x2{pack_bf16_rne(h[0], h[1]), pack_bf16_rne(h[2], h[3])};
             }
         }
     }
 }
 
-// Second kernel: out[t, n] for 16 columns n and every token.  The items
-// (expert, depth chunk) are dealt to the waves; each wave adds its weighted
-// products into sums of its own in LDS, which are added in wave order.
-template <bool FP4>
-__global__ __launch_bounds__(kFewWaves2 *kWave) void few_down_kernel(FewArgs a)
+// Second kernel: out[t, n] for 16 columns n and every token.  The items (an
+// expert, a part of its depth) are dealt to the waves in rotation and taken
+// 8 slots at a time, turn by turn, the operands of the next turns (two of
+// MXFP4, one of bf16) arriving while one is multiplied; each wave adds its weighted products into sums of
+// its own in LDS, which are added in wave order.  LDS: the sums, the waves'
+// columns, then the lists.
+constexpr int kItemSlots = 8;
+struct FewDownLds {
+    size_t columns, wts, slots, expert, begin, bytes;
+    __host__ __device__ FewDownLds(int waves, int T, int n, int A)
+    {
+        columns = (size_t)waves * T * 64;
+        wts = columns + (size_t)waves * kItemSlots * 512;
+        slots = wts + (size_t)n * 4;
+        expert = slots + (size_t)(n + (n & 1)) * 2;
+        begin = expert + (size_t)(A + (A & 1)) * 2;
+        bytes = begin + (size_t)(A + 1) * 2;
+    }
+};
+
+template <bool FP4, int WAVES>
+__global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
 {
-    extern __shared__ float sums[];            // [waves][T][16]
+    constexpr int G = FP4 ? 2 : 8;             // a turn
+    extern __shared__ u32x4 lds4[];
+    uint8_t *lds = reinterpret_cast<uint8_t *>(lds4);
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
-    const int n = a.T * a.k;
-    const FewLists ls(a.lists, n < a.L ? n : a.L);
+    const int n = a.T * a.k, A = n < a.L ? n : a.L;
+    const FewLists ls(a.lists, A);
+    const FewDownLds at(WAVES, a.T, n, A);
+    float *sums = reinterpret_cast<float *>(lds);                          // [waves][T][16]
+    float *wts = reinterpret_cast<float *>(lds + at.wts);                  // [n]
+    int16_t *slots = reinterpret_cast<int16_t *>(lds + at.slots);          // [n]
+    int16_t *expert = reinterpret_cast<int16_t *>(lds + at.expert);        // [A]
+    int16_t *begin = reinterpret_cast<int16_t *>(lds + at.begin);          // [A + 1]
+    const int active = ls.active[0];
+    for (int i = tid; i < n; i += WAVES * kWave) {
+        wts[i] = a.weights[i];
+        slots[i] = (int16_t)ls.slots[i];       // those behind the last one are not used
+    }
+    for (int i = tid; i <= A; i += WAVES * kWave) {
+        if (i < A) expert[i] = (int16_t)ls.expert[i];
+        begin[i] = (int16_t)ls.begin[i];
+    }
     float *mine = sums + (size_t)wave * a.T * 16;
     for (int i = lane; i < a.T * 16; i += kWave) mine[i] = 0.0f;
-    const int active = ls.active[0];
+    __syncthreads();
     const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int64_t rows = a.H - n0 < 16 ? a.H - n0 : 16;
-    const int chunks = (int)((a.I + kFewChunk - 1) / kFewChunk);
+    const int64_t rows_n = a.H - n0 < 16 ? a.H - n0 : 16;
+    const uint32_t I = (uint32_t)a.I;
+    // four items a wave where the experts with slots are few
+    const int turns = (int)((I + kTurn - 1) / kTurn);
+    int parts = active > 0 ? (4 * WAVES + active - 1) / active : 1;
+    parts = parts < turns ? parts : turns;
+    const int items = active * parts;
     const int c = lane & 15, g = lane >> 4;
-    for (int it = wave; it < active * chunks; it += kFewWaves2) {
-        const int ai = it / chunks;
-        const int64_t d0 = (int64_t)(it % chunks) * kFewChunk;
-        const int64_t d1 = d0 + kFewChunk < a.I ? d0 + kFewChunk : a.I;
-        const int e = ls.expert[ai];
-        const int begin = ls.begin[ai], count = ls.begin[ai + 1] - begin;
-        rsrc_t wq[1], ws[1];
-        few_weight_rows<FP4>(a.w2, a.w2_s, (int64_t)e * a.H + n0, rows, a.I, &wq[0], &ws[0]);
-        for (int c0 = 0; c0 < count; c0 += 16) {
-            const bool real = c0 + c < count;
-            const int slot = ls.slots[begin + (real ? c0 + c : c0)];
-            f32x4 acc[1] = {};
-            few_product<FP4, 1>(acc, wq, ws, a.h + (int64_t)slot * a.I, a.I, d0, d1, FewStep<FP4>::kDepth);
-            const float wt = real ? a.weights[slot] : 0.0f;
+    const rsrc_t hr = make_rsrc(a.h, (uint32_t)n * I * 2);
+    int most = 0;                              // slots of an expert
+    for (int i = 0; i < active; ++i) most = begin[i + 1] - begin[i] > most ? begin[i + 1] - begin[i] : most;
+
+    auto run = [&](auto rows2) {
+        constexpr int XT = decltype(rows2)::value;
+        struct Turn {
+            int begin, live;                   // its slots in the list
+            bool last;                         // of the item for these slots
+            uint32_t d;
+            FewWeights<FP4, 1, G> w;
+            FewColumns<XT> x;
+        };
+        // what is loaded next: item, its experts' slots, its turns
+        int it = wave - WAVES, count = 0, first = 0, c0 = 0, turn = 0, turn0 = 0, turn1 = 0;
+        FewRows<FP4> rows[1];
+        uint32_t x_off[XT];
+        auto set_slots = [&] {
+            const int live = count - c0 < kItemSlots ? count - c0 : kItemSlots;
+#pragma unroll
+            for (int j = 0; j < XT; ++j) {
+                const int i = 2 * j + (lane >> 5);
+                x_off[j] = live > 0 ? (uint32_t)slots[first + c0 + (i < live ? i : 0)] * I * 2 : 0u;
+            }
+            turn = turn0;
+        };
+        auto next_item = [&] {
+            it += WAVES;
+            c0 = 0;
+            if (it < items) {
+                const int ai = it / parts, part = it % parts;
+                const int e = __builtin_amdgcn_readfirstlane(expert[ai]);
+                first = __builtin_amdgcn_readfirstlane(begin[ai]);
+                count = __builtin_amdgcn_readfirstlane(begin[ai + 1]) - first;
+                turn0 = part * turns / parts;
+                turn1 = (part + 1) * turns / parts;
+                rows[0] = FewRows<FP4>(a.w2, a.w2_s, (int64_t)e * a.H + n0, rows_n, a.I);
+            } else {
+                count = 0;
+            }
+            set_slots();
+        };
+        // the next turn's operands; past the last item no memory is read and there are no slots
+        auto load = [&](Turn &q) {
+            q.begin = first + c0;
+            q.live = count - c0 < kItemSlots ? count - c0 : kItemSlots;
+            q.d = count ? (uint32_t)turn * kTurn : I;
+            q.last = turn + 1 == turn1;
+            q.x.lds = lds + at.columns + (size_t)wave * kItemSlots * 512;
+            q.x.load(hr, I, q.d, [&](int i) { return x_off[i / 2]; });
+            q.w.load(rows, I, q.d, 0);
+            if (++turn == turn1) {
+                c0 += kItemSlots;
+                if (c0 < count)
+                    set_slots();
+                else
+                    next_item();
+            }
+        };
+        f32x4 acc[1] = {};
+        auto finish = [&](Turn &q) {
+            q.x.store();
+            q.w.multiply(acc, I, q.d, 0, [&](uint32_t i) { return q.x.chunk(i); });
+            if (!q.last) return;
+            const bool real = c < q.live;
+            const int slot = slots[q.begin + (real ? c : 0)];
+            const float wt = wts[slot];
             const int t = slot / a.k;
-            // a token that names the expert twice has both slots side by
-            // side: the later ones add in a later round
+            // a token that names the expert more than once has those slots side
+            // by side: the later ones add in later rounds
+            const int prev = __builtin_amdgcn_update_dpp(-1, t, 0x111, 0xF, 0xF, false);       // row_shr:1
             int rank = 0;
-            for (int j = 1; j < 16; ++j) {
-                const int pt = __shfl(t, (lane & ~15) + (c >= j ? c - j : 0), kWave);
-                if (c >= j && pt == t) ++rank;
+            if (__ballot(real && prev == t) != 0) {
+                for (int j = 1; j < kItemSlots; ++j) {
+                    const int pt = __shfl(t, (lane & ~15) + (c >= j ? c - j : 0), kWave);
+                    if (c >= j && pt == t) ++rank;
+                }
             }
             for (int round = 0; __ballot(real && rank >= round) != 0; ++round) {
                 if (real && rank == round) {
@@ -1059,18 +1342,44 @@ __global__ __launch_bounds__(kFewWaves2 *kWave) void few_down_kernel(FewArgs a)
                     *o = *o + acc[0] * wt;
                 }
             }
+            acc[0] = f32x4{};
+        };
+        auto step = [&](Turn &q) {
+            if (q.live <= 0) return false;
+            finish(q);
+            __builtin_amdgcn_sched_barrier(0);
+            load(q);
+            __builtin_amdgcn_sched_barrier(0);
+            return true;
+        };
+        next_item();
+        Turn q0, q1;
+        load(q0);
+        load(q1);
+        if constexpr (FP4) {
+            Turn q2;
+            load(q2);
+            while (step(q0) && step(q1) && step(q2)) {
+            }
+        } else {
+            while (step(q0) && step(q1)) {
+            }
         }
-    }
+    };
+    if (most <= 2)
+        run(std::integral_constant<int, 1>{});
+    else
+        run(std::integral_constant<int, kItemSlots / 2>{});
     __syncthreads();
-    for (int i = tid; i < a.T * 8; i += kFewWaves2 * kWave) {
+    for (int i = tid; i < a.T * 8; i += WAVES * kWave) {
         const int t = i / 8, j = 2 * (i % 8);
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves2; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             s0 += sums[((size_t)w * a.T + t) * 16 + j];
             s1 += sums[((size_t)w * a.T + t) * 16 + j + 1];
         }
-        if (j < rows) *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.H + n0 + j) = pack_bf16_rne(s0, s1);
+        if (j < rows_n) *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.H + n0 + j) = pack_bf16_rne(s0, s1);
     }
 }
 
@@ -1152,6 +1461,8 @@ inline int check_few(int64_t T, int32_t k, int64_t H, int64_t I, int32_t L)
     if (rc != CDL_OK) return rc;
     if (H < 1 || I < 1 || L < 1 || L > CDL_MAX_LOCAL_EXPERTS) return CDL_ERR_BAD_SIZE;
     if (H > CDL_MAX_HIDDEN || I > CDL_MAX_HIDDEN) return CDL_ERR_TOO_LARGE;
+    // the token rows and the activations are addressed with 32-bit byte offsets
+    if (T * H > INT32_MAX - 8 || T * k * I > INT32_MAX - 8) return CDL_ERR_TOO_LARGE;
     if (T > CDL_MOE_LAYER_MAX_TOKENS || T * k > kFewMaxSlots) return CDL_ERR_UNSUPPORTED;
     return CDL_OK;
 }
@@ -1173,13 +1484,26 @@ int run_few(FewArgs a, void *ws, hipStream_t stream)
     const int n = a.T * a.k;
     a.lists = (int32_t *)ws;
     a.h = (uint16_t *)((uint8_t *)ws + few_list_bytes(a.T, a.k, a.L));
-    const size_t lds1 = (size_t)a.L * 4 + (size_t)n * 4 + (size_t)n * 2;
-    few_gate_up_kernel<FP4><<<dim3((unsigned)((a.I + 15) / 16), (unsigned)(n < a.L ? n : a.L)), dim3(kFewThreads),
-                              lds1, stream>>>(a);
+    const size_t lds1 = n > kWave ? (size_t)a.L * 4 + (size_t)n * 4 + (size_t)n * 2 : 0;
+    const int A = n < a.L ? n : a.L;
+    constexpr int CB = FP4 ? 2 : 1;
+    few_gate_up_kernel<FP4, CB><<<dim3((unsigned)((a.I + 16 * CB - 1) / (16 * CB)), (unsigned)A), dim3(kFewThreads),
+                                  lds1, stream>>>(a);
     int rc = launch_status();
     if (rc != CDL_OK) return rc;
-    few_down_kernel<FP4><<<dim3((unsigned)((a.H + 15) / 16)), dim3(kFewWaves2 * kWave),
-                           (size_t)kFewWaves2 * a.T * 64, stream>>>(a);
+    const dim3 grid((unsigned)((a.H + 15) / 16));
+    // Waves a workgroup: two workgroups a CU where there are that many, by what
+    // every wave's sums take of the LDS; otherwise as many as fit.
+    static_assert(8 * CDL_MOE_LAYER_MAX_TOKENS * 64 + 8 * kItemSlots * 512 + kFewMaxSlots * 10 + 16 <= 160 * 1024 &&
+                      16 * 64 * 64 + 16 * kItemSlots * 512 + 2048 * 10 + 16 <= 160 * 1024,
+                  "the second kernel's LDS");
+    const bool many = grid.x >= 256;
+    if (!many && a.T <= 64 && n <= 2048)
+        few_down_kernel<FP4, 16><<<grid, dim3(16 * kWave), FewDownLds(16, a.T, n, A).bytes, stream>>>(a);
+    else if (!many || a.T <= 64)
+        few_down_kernel<FP4, 8><<<grid, dim3(8 * kWave), FewDownLds(8, a.T, n, A).bytes, stream>>>(a);
+    else
+        few_down_kernel<FP4, 4><<<grid, dim3(4 * kWave), FewDownLds(4, a.T, n, A).bytes, stream>>>(a);
     return launch_status();
 }
 
