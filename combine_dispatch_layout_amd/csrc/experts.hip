@@ -826,9 +826,13 @@ struct FewArgs {
     uint16_t *h;                 // [T k, I]
 };
 
+// Up to 64 slots, the routing lists hold the experts with slots in the order
+// of their first slot; above, all L experts.
+__host__ __device__ inline int few_experts(int n, int L) { return n > kWave ? L : n < L ? n : L; }
+
 // Routing lists in the workspace, written by the first kernel: the number of
-// experts with slots, then for the a-th of them its index and the begin of
-// its slots, then the slots (flat t * k + j, ascending within an expert).
+// experts listed, then for the a-th of them its index and the begin of its
+// slots, then the slots (flat t * k + j, ascending within an expert).
 struct FewLists {
     int32_t *active, *expert, *begin, *slots;
     __host__ __device__ FewLists(int32_t *p, int A) : active(p), expert(p + 4), begin(p + 4 + A), slots(p + 4 + 2 * A + 4) {}
@@ -887,6 +891,7 @@ struct FewWeights {
     uint32_t at[NW];                           // byte of the lane's first scale in its words, at % 4
 
     // steps from `first` on of the turn at element d; past `depth` no memory is read
+    template <bool SCALES>
     __device__ __forceinline__ void load(const FewRows<FP4> (&rows)[NW], uint32_t depth, uint32_t d, int first)
     {
         const uint32_t lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
@@ -897,7 +902,7 @@ struct FewWeights {
 #pragma unroll
             for (int n = 0; n < NW; ++n) w[j][n] = buf_ld16(rows[n].q, off, 0);
         }
-        if constexpr (FP4) {
+        if constexpr (FP4 && SCALES) {
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
                 at[n] = rows[n].shift + r * (depth / 32) + d / 32 + 2 * g;
@@ -905,16 +910,19 @@ struct FewWeights {
             }
         }
     }
+    // the lane's two scale bytes of block n
+    __device__ __forceinline__ uint32_t scales(int n) const { return __builtin_amdgcn_alignbyte(s[n].y, s[n].x, at[n] & 3u); }
     // acc[n] += block n * columns; column(chunk) is the lane's column's 8
-    // elements from 8 chunk on of the turn
-    template <typename F>
-    __device__ __forceinline__ void multiply(f32x4 (&acc)[NW], uint32_t depth, uint32_t d, int first, F &&column)
+    // elements from 8 chunk on of the turn, scale(n) the lane's two scale bytes
+    // of block n
+    template <typename F, typename S>
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[NW], uint32_t depth, uint32_t d, int first, F &&column, S &&scale)
     {
         const uint32_t lane = threadIdx.x & (kWave - 1), g = lane >> 4;
         if constexpr (FP4) {
             uint32_t bytes[NW];
 #pragma unroll
-            for (int n = 0; n < NW; ++n) bytes[n] = __builtin_amdgcn_alignbyte(s[n].y, s[n].x, at[n] & 3u);
+            for (int n = 0; n < NW; ++n) bytes[n] = scale(n);
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 v8bf16 b[4];
@@ -951,11 +959,10 @@ struct FewWeights {
 };
 
 // A turn of up to 2 XT bf16 rows, the columns of the product, on its way
-// through a wave's own 16 x 512 bytes of LDS: a load brings two rows (32 lanes
+// through a wave's own 2 XT x 512 bytes of LDS: a load brings two rows (32 lanes
 // of 16 bytes each), where fragments straight from memory would take a load
 // of 64 lanes for every 32 elements whatever the number of rows.  16-byte
 // chunk q of row r lies at q ^ r.
-constexpr int kColumnBytes = 16 * 512;
 template <int XT>
 struct FewColumns {
     u32x4 v[XT];
@@ -991,31 +998,49 @@ struct FewColumns {
 
 __device__ __forceinline__ uint64_t lanes_below(int lane) { return lane ? ~0ull >> (kWave - lane) : 0ull; }
 
-// First kernel: h[slot, i] = silu(gate) * up for 16 CB columns i of the a-th
-// expert with slots (blockIdx.y); blockIdx.x is the column tile.  The 4 waves
-// take the turns of the depth in rotation, a part of a turn being multiplied
-// while the next one arrives, and add their sums in LDS.
-template <bool FP4, int CB>
+// First kernel: h[slot, i] = silu(gate) * up for 16 columns i of the a-th
+// listed expert (blockIdx.y); blockIdx.x is the column tile.  The 4 waves take
+// the turns of the depth in rotation, a part of a turn being multiplied while
+// the next one arrives, and add their sums in LDS.  LDS_SCALES: MXFP4 scales
+// of the whole depth lie in LDS.
+template <bool FP4, int XT, bool LDS_SCALES>
 __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
 {
-    constexpr int NW = 2 * CB;
-    extern __shared__ int32_t lds[];
-    int32_t *hist = lds;                       // [L]
-    int32_t *list = lds + a.L;                 // [n] the expert's slots
-    int16_t *es = reinterpret_cast<int16_t *>(list + a.T * a.k);   // [n] local expert of each slot
+    constexpr int NW = 2, kSlots = 2 * XT;     // a gate and an up block; slots at a time
+    constexpr int G = FP4 ? 2 : 4;
+    extern __shared__ u32x4 lds4[];
+    int16_t *list = reinterpret_cast<int16_t *>(lds4);             // [n] the expert's slots (n > 64)
     __shared__ f32x4 part[kFewWaves][NW][kWave];
-    __shared__ u32x4 columns[kFewWaves][kColumnBytes / 16];
+    __shared__ u32x4 columns[kFewWaves][kSlots * 512 / 16];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
     const int n = a.T * a.k;
-    const FewLists ls(a.lists, n < a.L ? n : a.L);
+    const FewLists ls(a.lists, few_experts(n, a.L));
+    // every expert's first workgroup writes the expert's own list
     const bool publish = blockIdx.x == 0 && wave == 0;
-    int mine = -1, count = 0, one_slot = 0;
+    int mine = -1, count = 0, before = 0, one_slot = 0;
+    const int c = lane & 15, g = lane >> 4;
+    const uint32_t H = (uint32_t)a.H;
+    const int64_t i0 = (int64_t)blockIdx.x * 16;
+    const int64_t live_i = a.I - i0 < 16 ? a.I - i0 : 16;
+    constexpr bool kLdsScales = FP4 && LDS_SCALES;
+    FewRows<FP4> rows[NW];
+    FewWeights<FP4, NW, G> w[2];
+    auto set_rows = [&] {
+        mine = __builtin_amdgcn_readfirstlane(mine);
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            rows[i] = FewRows<FP4>(a.w13, a.w13_s, (int64_t)mine * 2 * a.I + i * a.I + i0, live_i, a.H);
+    };
+    auto load_w = [&](FewWeights<FP4, NW, G> &t, uint32_t at, int first) {
+        t.template load<!kLdsScales>(rows, H, at, first);
+    };
+    bool ahead = false;                        // the first weights are on their way
+    // every wave finds the expert's slots by itself
     if (n <= kWave) {
-        // every wave finds the expert by itself: slot i lies in lane i, the
-        // experts in the order of their first slots
+        // slot i lies in lane i
         const int e = lane < n ? local_expert(a.ids[lane], a.expert_begin, a.L) : -1;
         uint64_t left = __ballot(e >= 0), mask = 0;
-        int a_th = 0, before = 0;
+        int a_th = 0;
         while (left) {
             const int el = __builtin_amdgcn_readlane(e, (int)__builtin_ctzll(left));
             const uint64_t m = __ballot(e == el);
@@ -1028,18 +1053,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
             left &= ~m;
         }
         count = __popcll(mask);
-        if (publish) {
-            if (lane == 0) {
-                if (blockIdx.y == 0) ls.active[0] = a_th;
-                if (mine >= 0) {
-                    ls.expert[blockIdx.y] = mine;
-                    ls.begin[blockIdx.y] = before;
-                    ls.begin[blockIdx.y + 1] = before + count;
-                }
-            }
-            if (mask >> lane & 1) ls.slots[before + __popcll(mask & lanes_below(lane))] = lane;
-        }
-        if (mine < 0) return;
+        if (publish && lane == 0 && blockIdx.y == 0) ls.active[0] = a_th;
+        if (publish && (mask >> lane & 1)) ls.slots[before + __popcll(mask & lanes_below(lane))] = lane;
         // lane i takes the expert's i-th slot
         int at = 0;
         for (uint64_t m = mask; m; m &= m - 1, ++at) {
@@ -1047,82 +1062,65 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
             if (at == lane) one_slot = slot;
         }
     } else {
-        for (int e = tid; e < a.L; e += kFewThreads) hist[e] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kFewThreads) {
-            const int e = local_expert(a.ids[i], a.expert_begin, a.L);
-            es[i] = (int16_t)e;
-            if (e >= 0) atomicAdd(&hist[e], 1);
-        }
-        __syncthreads();
-        // the blockIdx.y-th expert with slots, and the slots of those before it
-        int seen = 0, before = 0;
-        int32_t slots_seen = 0;
-        for (int e0 = 0; e0 < a.L; e0 += kWave) {
-            const int32_t c = e0 + lane < a.L ? hist[e0 + lane] : 0;
-            const uint64_t m = __ballot(c > 0);
-            const int rank = seen + __popcll(m & lanes_below(lane));
-            const int32_t incl = slots_seen + wave_inclusive_scan(c);
-            const uint64_t hit = __ballot(c > 0 && rank == (int)blockIdx.y);
-            if (hit) {
-                const int l = (int)__builtin_ctzll(hit);
-                mine = e0 + l;
-                before = __builtin_amdgcn_readlane(incl - c, l);
-            }
-            seen += __popcll(m);
-            slots_seen = __builtin_amdgcn_readlane(incl, kWave - 1);
-        }
-        // every expert's first workgroup writes the expert's own list
-        if (publish && lane == 0) {
-            if (blockIdx.y == 0) ls.active[0] = seen;
-            if (mine >= 0) {
-                ls.expert[blockIdx.y] = mine;
-                ls.begin[blockIdx.y] = before;
-                ls.begin[blockIdx.y + 1] = before + hist[mine];
-            }
-        }
-        if (mine < 0) return;
-        if (wave == 0) {
-            int at = 0;
-            for (int i0 = 0; i0 < n; i0 += kWave) {
-                const bool is = i0 + lane < n && es[i0 + lane] == mine;
-                const uint64_t m = __ballot(is);
-                if (is) {
-                    const int to = at + __popcll(m & lanes_below(lane));
-                    list[to] = i0 + lane;
-                    if (publish) ls.slots[before + to] = i0 + lane;
-                }
-                at += __popcll(m);
-            }
-        }
-        count = hist[mine];
-        __syncthreads();
-    }
-    mine = __builtin_amdgcn_readfirstlane(mine);
-    const int64_t i0 = (int64_t)blockIdx.x * 16 * CB;
-    FewRows<FP4> rows[NW];                     // gate blocks, then up blocks
+        // the expert is known: its first weights are loaded behind the first ids
+        // where there are slots for most experts
+        mine = (int)blockIdx.y;
+        constexpr int kBatch = 8;
+        int32_t id[kBatch];
+        auto load_ids = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        const int64_t c = i0 + i % CB * 16, left = a.I - c;
-        rows[i] = FewRows<FP4>(a.w13, a.w13_s, (int64_t)mine * 2 * a.I + i / CB * a.I + (left > 0 ? c : 0),
-                               left < 16 ? left : 16, a.H);
+            for (int q = 0; q < kBatch; ++q) {
+                const int i = s0 + q * kWave + lane;
+                id[q] = a.ids[i < n ? i : 0];
+            }
+        };
+        load_ids(0);
+        set_rows();
+        ahead = n >= a.L;
+        if (ahead) load_w(w[0], (uint32_t)wave * kTurn, 0);
+        // all waves write the same list
+        for (int s0 = 0; s0 < n; s0 += kBatch * kWave) {
+            if (s0) load_ids(s0);
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int i = s0 + q * kWave + lane;
+                const int e = i < n ? local_expert(id[q], a.expert_begin, a.L) : -1;
+                const uint64_t m = __ballot(e == mine);
+                if (e == mine) {
+                    const int to = count + __popcll(m & lanes_below(lane));
+                    list[to] = (int16_t)i;
+                }
+                count += __popcll(m);
+                before += __popcll(__ballot(e >= 0 && e < mine));
+            }
+        }
+        if (publish) {
+            if (lane == 0 && blockIdx.y == 0) ls.active[0] = a.L;
+            for (int i = lane; i < count; i += kWave) ls.slots[before + i] = list[i];
+        }
     }
-    const int c = lane & 15, g = lane >> 4;
-    const uint32_t H = (uint32_t)a.H;
+    if (publish && lane == 0 && mine >= 0) {
+        ls.expert[blockIdx.y] = mine;
+        ls.begin[blockIdx.y] = before;
+        ls.begin[blockIdx.y + 1] = before + count;
+    }
+    if (count == 0) return;
+    if (n <= kWave) set_rows();
     const rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.T * a.H * 2));
+    // The scales of a block's 16 rows are one run of bytes: they are brought to
+    // LDS whole, where a load per turn would fetch every row's line again.
+    uint8_t *scales = reinterpret_cast<uint8_t *>(lds4) + (n > kWave ? (n * 2 + 15) / 16 * 16 : 0);
+    const uint32_t run = H / 2, pitch = (run + 3 + 3) & ~3u;       // bytes of a run, and with its first word's shift
     auto slot_of = [&](int i) {                // the expert's i-th slot
-        return n <= kWave ? __shfl(one_slot, i, kWave) : list[i];
+        return n <= kWave ? __shfl(one_slot, i, kWave) : (int)list[i];
     };
-    for (int c0 = 0; c0 < count; c0 += 16) {
-        const int live = count - c0 < 16 ? count - c0 : 16;
+    for (int c0 = 0; c0 < count; c0 += kSlots) {
+        const int live = count - c0 < kSlots ? count - c0 : kSlots;
         const int slot = slot_of(c0 + (c < live ? c : 0));
         f32x4 acc[NW] = {};
-        uint8_t *mine_lds = reinterpret_cast<uint8_t *>(columns[wave]);
-        auto product = [&](auto rows2) {
-            constexpr int XT = decltype(rows2)::value;
-            constexpr int G = FP4 ? 2 : 4;
+        {
             FewColumns<XT> x;
-            x.lds = mine_lds;
+            x.lds = reinterpret_cast<uint8_t *>(columns[wave]);
             uint32_t off[XT];
 #pragma unroll
             for (int j = 0; j < XT; ++j) {
@@ -1131,25 +1129,41 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
             }
             auto load_x = [&](uint32_t d) { x.load(xr, H, d, [&](int i) { return off[i / 2]; }); };
             auto column = [&](uint32_t q) { return x.chunk(q); };
-            FewWeights<FP4, NW, G> w[2];
+            auto multiply = [&](FewWeights<FP4, NW, G> &t, uint32_t at, int first) {
+                t.multiply(acc, H, at, first, column, [&](int b) -> uint32_t {
+                    if constexpr (!kLdsScales) return t.scales(b);
+                    // (a turn's last groups may lie past the row's end: read, not used)
+                    const uint8_t *p = scales + b * pitch + rows[b].shift + c * (H / 32) + (at < H ? at / 32 + 2 * g : 0);
+                    return (uint32_t)p[0] | (uint32_t)p[1] << 8;
+                });
+            };
             constexpr uint32_t kNext = kTurn * kFewWaves;
             uint32_t d = (uint32_t)wave * kTurn;
             load_x(d);
-            w[0].load(rows, H, d, 0);
+            if (c0 || !ahead) load_w(w[0], d, 0);
+            if constexpr (kLdsScales) {
+                if (c0 == 0) {
+                    for (uint32_t i = (uint32_t)tid * 4; i < pitch; i += kFewThreads * 4)
+#pragma unroll
+                        for (int b = 0; b < NW; ++b)
+                            *reinterpret_cast<int32_t *>(scales + b * pitch + i) = buf_ld4(rows[b].s, i, 0);
+                    __syncthreads();
+                }
+            }
             x.store();
             load_x(d + kNext);
             if constexpr (FP4) {
                 // a part is a turn
                 for (; d < H; d += 2 * kNext) {
-                    w[1].load(rows, H, d + kNext, 0);
+                    load_w(w[1], d + kNext, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    w[0].multiply(acc, H, d, 0, column);
+                    multiply(w[0], d, 0);
                     x.store();
                     load_x(d + 2 * kNext);
                     __builtin_amdgcn_sched_barrier(0);
-                    w[0].load(rows, H, d + 2 * kNext, 0);
+                    load_w(w[0], d + 2 * kNext, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    w[1].multiply(acc, H, d + kNext, 0, column);
+                    multiply(w[1], d + kNext, 0);
                     x.store();
                     load_x(d + 3 * kNext);
                     __builtin_amdgcn_sched_barrier(0);
@@ -1157,45 +1171,35 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
             } else {
                 // a part is half a turn
                 for (; d < H; d += kNext) {
-                    w[1].load(rows, H, d, 4);
+                    load_w(w[1], d, 4);
                     __builtin_amdgcn_sched_barrier(0);
-                    w[0].multiply(acc, H, d, 0, column);
+                    multiply(w[0], d, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    w[0].load(rows, H, d + kNext, 0);
+                    load_w(w[0], d + kNext, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    w[1].multiply(acc, H, d, 4, column);
+                    multiply(w[1], d, 4);
                     x.store();
                     load_x(d + 2 * kNext);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-        };
-        if (live <= 2)
-            product(std::integral_constant<int, 1>{});
-        else if (live <= 4)
-            product(std::integral_constant<int, 2>{});
-        else if (live <= 8)
-            product(std::integral_constant<int, 4>{});
-        else
-            product(std::integral_constant<int, 8>{});
+        }
         if (c0) __syncthreads();               // the sums of the round before are read
 #pragma unroll
         for (int i = 0; i < NW; ++i) part[wave][i][lane] = acc[i];
         __syncthreads();
-        // wave b adds column block b
-        if (wave < CB) {
-            f32x4 gate = part[0][wave][lane], up = part[0][CB + wave][lane];
+        if (wave == 0) {
+            f32x4 gate = part[0][0][lane], up = part[0][1][lane];
 #pragma unroll
             for (int w = 1; w < kFewWaves; ++w) {
-                gate += part[w][wave][lane];
-                up += part[w][CB + wave][lane];
+                gate += part[w][0][lane];
+                up += part[w][1][lane];
             }
-            const int64_t col0 = i0 + wave * 16 + 4 * g;
-            if (c < live && col0 < a.I) {
+            if (c < live && 4 * g < live_i) {
                 float h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i];
-                *reinterpret_cast<u32x2 *>(a.h + (int64_t)slot * a.I + col0) =
+                *reinterpret_cast<u32x2 *>(a.h + (int64_t)slot * a.I + i0 + 4 * g) =
                     u32x2{pack_bf16_rne(h[0], h[1]), pack_bf16_rne(h[2], h[3])};
             }
         }
@@ -1229,7 +1233,7 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
     extern __shared__ u32x4 lds4[];
     uint8_t *lds = reinterpret_cast<uint8_t *>(lds4);
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
-    const int n = a.T * a.k, A = n < a.L ? n : a.L;
+    const int n = a.T * a.k, A = few_experts(n, a.L);
     const FewLists ls(a.lists, A);
     const FewDownLds at(WAVES, a.T, n, A);
     float *sums = reinterpret_cast<float *>(lds);                          // [waves][T][16]
@@ -1252,15 +1256,20 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t rows_n = a.H - n0 < 16 ? a.H - n0 : 16;
     const uint32_t I = (uint32_t)a.I;
+    int with_slots = 0;
+    bool many = false;                         // an expert with more than 2
+    for (int i0 = 0; i0 < active; i0 += kWave) {
+        const int have = i0 + lane < active ? begin[i0 + lane + 1] - begin[i0 + lane] : 0;
+        with_slots += __popcll(__ballot(have > 0));
+        many |= __ballot(have > 2) != 0;
+    }
     // four items a wave where the experts with slots are few
     const int turns = (int)((I + kTurn - 1) / kTurn);
-    int parts = active > 0 ? (4 * WAVES + active - 1) / active : 1;
+    int parts = with_slots > 0 ? (4 * WAVES + with_slots - 1) / with_slots : 1;
     parts = parts < turns ? parts : turns;
     const int items = active * parts;
     const int c = lane & 15, g = lane >> 4;
     const rsrc_t hr = make_rsrc(a.h, (uint32_t)n * I * 2);
-    int most = 0;                              // slots of an expert
-    for (int i = 0; i < active; ++i) most = begin[i + 1] - begin[i] > most ? begin[i + 1] - begin[i] : most;
 
     auto run = [&](auto rows2) {
         constexpr int XT = decltype(rows2)::value;
@@ -1273,7 +1282,8 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
         };
         // what is loaded next: item, its experts' slots, its turns
         int it = wave - WAVES, count = 0, first = 0, c0 = 0, turn = 0, turn0 = 0, turn1 = 0;
-        FewRows<FP4> rows[1];
+        // (a wave without an item loads through this empty descriptor)
+        FewRows<FP4> rows[1] = {FewRows<FP4>(a.w2, a.w2_s, 0, 0, a.I)};
         uint32_t x_off[XT];
         auto set_slots = [&] {
             const int live = count - c0 < kItemSlots ? count - c0 : kItemSlots;
@@ -1285,18 +1295,17 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             turn = turn0;
         };
         auto next_item = [&] {
-            it += WAVES;
-            c0 = 0;
-            if (it < items) {
-                const int ai = it / parts, part = it % parts;
-                const int e = __builtin_amdgcn_readfirstlane(expert[ai]);
+            count = c0 = 0;
+            for (it += WAVES; it < items; it += WAVES) {           // (experts without slots: none)
+                const int ai = it / parts;
                 first = __builtin_amdgcn_readfirstlane(begin[ai]);
                 count = __builtin_amdgcn_readfirstlane(begin[ai + 1]) - first;
+                if (count == 0) continue;
+                const int e = __builtin_amdgcn_readfirstlane(expert[ai]), part = it % parts;
                 turn0 = part * turns / parts;
                 turn1 = (part + 1) * turns / parts;
                 rows[0] = FewRows<FP4>(a.w2, a.w2_s, (int64_t)e * a.H + n0, rows_n, a.I);
-            } else {
-                count = 0;
+                break;
             }
             set_slots();
         };
@@ -1308,7 +1317,7 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             q.last = turn + 1 == turn1;
             q.x.lds = lds + at.columns + (size_t)wave * kItemSlots * 512;
             q.x.load(hr, I, q.d, [&](int i) { return x_off[i / 2]; });
-            q.w.load(rows, I, q.d, 0);
+            q.w.template load<true>(rows, I, q.d, 0);
             if (++turn == turn1) {
                 c0 += kItemSlots;
                 if (c0 < count)
@@ -1320,7 +1329,7 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
         f32x4 acc[1] = {};
         auto finish = [&](Turn &q) {
             q.x.store();
-            q.w.multiply(acc, I, q.d, 0, [&](uint32_t i) { return q.x.chunk(i); });
+            q.w.multiply(acc, I, q.d, 0, [&](uint32_t i) { return q.x.chunk(i); }, [&](int i) { return q.w.scales(i); });
             if (!q.last) return;
             const bool real = c < q.live;
             const int slot = slots[q.begin + (real ? c : 0)];
@@ -1366,10 +1375,10 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             }
         }
     };
-    if (most <= 2)
-        run(std::integral_constant<int, 1>{});
-    else
+    if (many)
         run(std::integral_constant<int, kItemSlots / 2>{});
+    else
+        run(std::integral_constant<int, 1>{});
     __syncthreads();
     for (int i = tid; i < a.T * 8; i += WAVES * kWave) {
         const int t = i / 8, j = 2 * (i % 8);
@@ -1470,7 +1479,7 @@ inline int check_few(int64_t T, int32_t k, int64_t H, int64_t I, int32_t L)
 inline size_t few_list_bytes(int64_t T, int32_t k, int32_t L)
 {
     const int64_t n = T * k;
-    return (FewLists::ints(n < L ? n : L, n) * sizeof(int32_t) + 255) & ~(size_t)255;
+    return (FewLists::ints(few_experts((int)n, L), n) * sizeof(int32_t) + 255) & ~(size_t)255;
 }
 
 inline size_t few_ws_bytes(int64_t T, int32_t k, int64_t I, int32_t L)
@@ -1484,11 +1493,30 @@ int run_few(FewArgs a, void *ws, hipStream_t stream)
     const int n = a.T * a.k;
     a.lists = (int32_t *)ws;
     a.h = (uint16_t *)((uint8_t *)ws + few_list_bytes(a.T, a.k, a.L));
-    const size_t lds1 = n > kWave ? (size_t)a.L * 4 + (size_t)n * 4 + (size_t)n * 2 : 0;
-    const int A = n < a.L ? n : a.L;
-    constexpr int CB = FP4 ? 2 : 1;
-    few_gate_up_kernel<FP4, CB><<<dim3((unsigned)((a.I + 16 * CB - 1) / (16 * CB)), (unsigned)A), dim3(kFewThreads),
-                                  lds1, stream>>>(a);
+    const int A = few_experts(n, a.L);
+    const size_t lists = n > kWave ? ((size_t)n * 2 + 15) / 16 * 16 : 0;
+    const dim3 grid1((unsigned)((a.I + 15) / 16), (unsigned)A);
+    // scales of 32 rows in LDS (16 KB at H = 16384; one token, H = 7168, I =
+    // 2048, top-8: 31 -> 26 us)
+    const bool lds_scales = FP4 && a.H <= 16384;
+    const size_t lds1 = lists + (lds_scales ? 2 * ((size_t)a.H / 2 + 8) + 64 : 0);
+    auto launch = [&](auto xt, auto sc) {
+        few_gate_up_kernel<FP4, decltype(xt)::value, decltype(sc)::value><<<grid1, dim3(kFewThreads), lds1, stream>>>(a);
+    };
+    auto launch_xt = [&](auto sc) {
+        if (a.T <= 2)
+            launch(std::integral_constant<int, 1>{}, sc);
+        else
+            launch(std::integral_constant<int, 4>{}, sc);
+    };
+    if constexpr (FP4) {
+        if (lds_scales)
+            launch_xt(std::true_type{});
+        else
+            launch_xt(std::false_type{});
+    } else {
+        launch_xt(std::false_type{});
+    }
     int rc = launch_status();
     if (rc != CDL_OK) return rc;
     const dim3 grid((unsigned)((a.H + 15) / 16));
