@@ -68,42 +68,70 @@ __device__ __forceinline__ u32x2 mx_quant16(u32x4 a, u32x4 b, uint32_t *scale)
     return u32x2{q[0], q[1]};
 }
 
+__device__ __forceinline__ uint64_t lanes_below(int lane) { return lane ? ~0ull >> (kWave - lane) : 0ull; }
+
 constexpr int kMxPairs = 7;      // blocks of 1024 elements a wave holds: one row at H = 7168
 
-// A wave's row of H elements (from c0 = a multiple of 7 blocks on): loaded,
-// quantised and held; lane l of block p has elements 1024 p + 16 l to + 15.
-__device__ __forceinline__ void mx_load_row(u32x4 (&v)[2 * kMxPairs], rsrc_t xr, int lane, uint32_t byte0)
-{
-#pragma unroll
-    for (int p = 0; p < kMxPairs; ++p) {
-        v[2 * p] = buf_ld16(xr, (uint32_t)lane * 32u + p * 2048u + byte0, 0);
-        v[2 * p + 1] = buf_ld16(xr, (uint32_t)lane * 32u + p * 2048u + byte0 + 16u, 0);
-    }
-}
+// A wave's row from element `first` on (a multiple of 7 blocks), 7 blocks of
+// 1024 elements: lane l has elements 1024 p + 16 l to + 15 of block p, q[p]
+// their codes; the even lanes hold their groups' scale bytes in s[p].
+struct MxRow {
+    u32x2 q[kMxPairs];
+    uint32_t s[kMxPairs];
 
-__device__ __forceinline__ void mx_quant_row(const u32x4 (&v)[2 * kMxPairs], u32x2 (&q)[kMxPairs],
-                                             uint32_t (&s)[kMxPairs])
-{
+    __device__ __forceinline__ void load_quant(rsrc_t xr, int lane, uint32_t first)
+    {
+        u32x4 v[2 * kMxPairs];
 #pragma unroll
-    for (int p = 0; p < kMxPairs; ++p) q[p] = mx_quant16(v[2 * p], v[2 * p + 1], &s[p]);
-}
-
-// The held blocks to destination row dst.  The range check of the row's
-// descriptors drops the lanes past the row (H is a multiple of 32: a lane's
-// 8 bytes and its group's byte are inside the row or outside as a whole).
-__device__ __forceinline__ void mx_store_row(const u32x2 (&q)[kMxPairs], const uint32_t (&s)[kMxPairs],
-                                             int lane, uint8_t *oq, uint8_t *os, int64_t dst, int64_t H,
-                                             uint32_t block0)
-{
-    const rsrc_t rq = make_rsrc(oq + dst * (H / 2), (uint32_t)(H / 2));
-    const rsrc_t rs = make_rsrc(os + dst * (H / 32), (uint32_t)(H / 32));
+        for (int p = 0; p < kMxPairs; ++p) {
+            v[2 * p] = buf_ld16(xr, (uint32_t)lane * 32u + p * 2048u + first * 2u, 0);
+            v[2 * p + 1] = buf_ld16(xr, (uint32_t)lane * 32u + p * 2048u + first * 2u + 16u, 0);
+        }
 #pragma unroll
-    for (int p = 0; p < kMxPairs; ++p) {
-        if ((int64_t)(block0 + p) * 1024 >= H) break;
-        __builtin_amdgcn_raw_buffer_store_b64(q[p], rq, (uint32_t)lane * 8u + (block0 + p) * 512u, 0, 0);
-        if ((lane & 1) == 0)
-            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)s[p], rs, (uint32_t)lane / 2 + (block0 + p) * 32u, 0, 0);
+        for (int p = 0; p < kMxPairs; ++p) q[p] = mx_quant16(v[2 * p], v[2 * p + 1], &s[p]);
     }
+
+    // The scales as words (four bytes of neighbouring groups): lane 8 d + p
+    // takes word d of block p, so that all of them leave in one store.
+    __device__ __forceinline__ uint32_t scale_words(int lane) const
+    {
+        uint32_t mine = 0;
+#pragma unroll
+        for (int p = 0; p < kMxPairs; ++p) {
+            const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s[p], 0x00, 0xF, 0xF, false);   // quad_perm [0,0,0,0]
+            const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s[p], 0xAA, 0xF, 0xF, false);   // quad_perm [2,2,2,2]
+            const uint32_t w = lo | hi << 8;
+            const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x141, 0xF, 0xF, false);      // row_half_mirror
+            const uint32_t word = lane & 4 ? o | w << 16 : w | o << 16;
+            mine = (lane & 7) == p ? word : mine;
+        }
+        return mine;
+    }
+
+    // To row dst.  The range check of the row's descriptors drops the lanes
+    // past the row (H is a multiple of 32: a lane's 8 bytes and its group's
+    // byte are inside the row or outside as a whole).  words: scale rows are
+    // word-aligned, and `sw` is scale_words().
+    __device__ __forceinline__ void store(int lane, uint8_t *oq, uint8_t *os, int64_t dst, int64_t H, uint32_t first,
+                                          bool words, uint32_t sw) const
+    {
+        const rsrc_t rq = make_rsrc(oq + dst * (H / 2), (uint32_t)(H / 2));
+        const rsrc_t rs = make_rsrc(os + dst * (H / 32), (uint32_t)(H / 32));
+#pragma unroll
+        for (int p = 0; p < kMxPairs; ++p) {
+            if ((int64_t)first + p * 1024 >= H) break;
+            __builtin_amdgcn_raw_buffer_store_b64(q[p], rq, (uint32_t)lane * 8u + p * 512u + first / 2, 0, 0);
+            if (!words && (lane & 1) == 0)
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)s[p], rs, (uint32_t)lane / 2 + p * 32u + first / 32, 0, 0);
+        }
+        if (words && (lane & 7) < kMxPairs)
+            __builtin_amdgcn_raw_buffer_store_b32(sw, rs, (uint32_t)((lane & 7) * 8 + (lane >> 3)) * 4u + first / 32, 0, 0);
+    }
+};
+
+__device__ __forceinline__ bool mx_scale_rows_aligned(const uint8_t *os, int64_t H)
+{
+    return (H / 32) % 4 == 0 && ((uintptr_t)os & 3) == 0;
 }
 
 constexpr int kMxRowsPerWg = 4;      // rows (waves) per workgroup
@@ -113,39 +141,65 @@ __global__ __launch_bounds__(kMxRowsPerWg *kWave) void mx_quant_kernel(
     const uint16_t *__restrict__ x, int64_t rows, int64_t H, uint8_t *__restrict__ q, uint8_t *__restrict__ s)
 {
     const int lane = threadIdx.x & (kWave - 1);
+    const bool words = mx_scale_rows_aligned(s, H);
     for (int64_t r = (int64_t)blockIdx.x * kMxRowsPerWg + wave_id(); r < rows;
          r += (int64_t)gridDim.x * kMxRowsPerWg) {
         const rsrc_t xr = make_rsrc(x + r * H, (uint32_t)(H * 2));
-        for (uint32_t b0 = 0; (int64_t)b0 * 1024 < H; b0 += kMxPairs) {
-            u32x4 v[2 * kMxPairs];
-            u32x2 c[kMxPairs];
-            uint32_t sc[kMxPairs];
-            mx_load_row(v, xr, lane, b0 * 2048u);
-            mx_quant_row(v, c, sc);
-            mx_store_row(c, sc, lane, q, s, r, H, b0);
+        for (uint32_t first = 0; (int64_t)first < H; first += kMxPairs * 1024) {
+            MxRow row;
+            row.load_quant(xr, lane, first);
+            row.store(lane, q, s, r, H, first, words, words ? row.scale_words(lane) : 0u);
         }
     }
 }
 
 // Codes back to bf16 (exact: three significant bits, exponents in bf16's
-// range; 6 * 2^127 and 4 * 2^126 overflow to infinity).  16 elements a thread.
-__global__ __launch_bounds__(256) void mx_dequant_kernel(const u32x2 *__restrict__ q, const uint8_t *__restrict__ s,
-                                                         int64_t n16, u32x4 *__restrict__ out)
+// range; 6 * 2^127 and 4 * 2^126 overflow to infinity).  8 elements a thread
+// and step, so that a wave stores 1 KB of a row at once.
+constexpr int kMxDequantSteps = 4;
+__global__ __launch_bounds__(256) void mx_dequant_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ s,
+                                                         int64_t n8, u32x4 *__restrict__ out)
 {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256) {
-        const u32x2 c = q[i];
-        const float p = __uint_as_float((uint32_t)s[i >> 1] << 23);
-        uint32_t o[8];
+    for (int64_t i0 = (int64_t)blockIdx.x * (256 * kMxDequantSteps) + threadIdx.x; i0 < n8;
+         i0 += (int64_t)gridDim.x * (256 * kMxDequantSteps)) {
+        uint32_t c[kMxDequantSteps], e[kMxDequantSteps];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t w = h ? c.y : c.x;
-            o[4 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p, 0));
-            o[4 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p, 1));
-            o[4 * h + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p, 2));
-            o[4 * h + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, p, 3));
+        for (int j = 0; j < kMxDequantSteps; ++j) {
+            const int64_t i = i0 + j * 256;
+            c[j] = i < n8 ? q[i] : 0u;
+            e[j] = i < n8 ? s[i >> 2] : 0u;
         }
-        out[2 * i] = u32x4{o[0], o[1], o[2], o[3]};
-        out[2 * i + 1] = u32x4{o[4], o[5], o[6], o[7]};
+#pragma unroll
+        for (int j = 0; j < kMxDequantSteps; ++j) {
+            const int64_t i = i0 + j * 256;
+            const float p = __uint_as_float(e[j] << 23);
+            const u32x4 o = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], p, 0)),
+                             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], p, 1)),
+                             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], p, 2)),
+                             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], p, 3))};
+            if (i < n8) __builtin_nontemporal_store(o, out + i);
+        }
+    }
+}
+
+// Token t's row to the destinations in dmask (lane j holds slot j's): the
+// part already held, when there is one, then the others.
+__device__ __forceinline__ void mx_store_token(const uint16_t *x, int64_t t, int64_t H, int lane, uint8_t *oq,
+                                               uint8_t *os, int32_t d, uint64_t dmask, uint32_t next, const MxRow *held)
+{
+    if (dmask == 0) return;
+    const bool words = mx_scale_rows_aligned(os, H);
+    auto store = [&](const MxRow &row, uint32_t first) {
+        const uint32_t sw = words ? row.scale_words(lane) : 0u;
+        for (uint64_t m = dmask; m; m &= m - 1)
+            row.store(lane, oq, os, __builtin_amdgcn_readlane(d, (int)__builtin_ctzll(m)), H, first, words, sw);
+    };
+    if (held) store(*held, 0);
+    const rsrc_t xr = make_rsrc(x + t * H, (uint32_t)(H * 2));
+    for (; (int64_t)next < H; next += kMxPairs * 1024) {
+        MxRow row;
+        row.load_quant(xr, lane, next);
+        store(row, next);
     }
 }
 
@@ -198,20 +252,139 @@ __global__ __launch_bounds__(kMxRowsPerWg *kWave) void mx_scatter_kernel(
         if (__ballot(drop) != 0 && lane == 0) set_status(status, CDL_STATUS_ROWS_OVERFLOW);
         if (drop) d = -1;
     }
-    const uint64_t dmask = __ballot(d >= 0);
-    if (dmask == 0) return;
-    const rsrc_t xr = make_rsrc(x + t * H, (uint32_t)(H * 2));
-    for (uint32_t b0 = 0; (int64_t)b0 * 1024 < H; b0 += kMxPairs) {
-        u32x4 v[2 * kMxPairs];
-        u32x2 c[kMxPairs];
-        uint32_t sc[kMxPairs];
-        mx_load_row(v, xr, lane, b0 * 2048u);
-        mx_quant_row(v, c, sc);
-        for (uint64_t m = dmask; m; m &= m - 1) {
-            const int32_t dst = __builtin_amdgcn_readlane(d, (int)__builtin_ctzll(m));
-            mx_store_row(c, sc, lane, oq, os, dst, H, b0);
+    mx_store_token(x, t, H, lane, oq, os, d, __ballot(d >= 0), 0, nullptr);
+}
+
+// One wave's layout of a small batch without superblock counts: as
+// layout_one_wave, with every slot counted here; tot[] is left holding the
+// experts' first rows.
+template <int TPB>
+__device__ __forceinline__ void mx_layout_self(const PermuteArgs &a, int64_t blk, int32_t *tot, int32_t *cur,
+                                               int32_t *dsts)
+{
+    constexpr int kLB = 16;
+    const int L = a.L, k = a.k, lane = threadIdx.x & (kWave - 1);
+    const int n = (int)(a.T * k);
+    const int64_t t_end = (blk + 1) * TPB < a.T ? (blk + 1) * TPB : a.T;
+    const int begin = (int)(blk * TPB * k), end = (int)(t_end * k);
+    const rsrc_t r_ids = make_rsrc(a.ids, (uint32_t)n * 4u);
+    int32_t my[TPB];
+#pragma unroll
+    for (int r = 0; r < TPB; ++r) my[r] = buf_ld4(r_ids, (uint32_t)(begin + r * kWave + lane) * 4u, 0);
+    for (int e = lane; e < L; e += kWave) tot[e] = cur[e] = 0;
+    for (int b0 = 0; b0 < n; b0 += kWave * kLB) {
+        int32_t id[kLB];
+#pragma unroll
+        for (int q = 0; q < kLB; ++q) id[q] = buf_ld4(r_ids, (uint32_t)(b0 + q * kWave + lane) * 4u, 0);
+#pragma unroll
+        for (int q = 0; q < kLB; ++q) {
+            const int i = b0 + q * kWave + lane;
+            const int32_t e = i < n ? local_expert(id[q], a.expert_begin, L) : -1;
+            if (e >= 0) {
+                atomicAdd(&tot[e], 1);
+                if (i < begin) atomicAdd(&cur[e], 1);
+            }
         }
     }
+    // the experts' padded offsets; workgroup 0 publishes, the padding rows are shared out
+    const int A = a.alignment;
+    const int nblk = (int)((a.T + TPB - 1) / TPB);
+    int32_t base = 0;
+    for (int e0 = 0; e0 < L; e0 += kWave) {
+        const int e = e0 + lane;
+        const int32_t cnt = e < L ? tot[e] : 0;
+        const int32_t padded = (cnt + A - 1) / A * A;
+        const int32_t incl = wave_inclusive_scan(padded);
+        const int32_t excl = base + incl - padded;
+        if (e < L) {
+            if (blk == 0) {
+                a.counts[e] = cnt;
+                a.seg_indptr[e] = excl;
+                if (a.masked_m) a.masked_m[e] = (int32_t)(cnt < a.ll_cap ? cnt : a.ll_cap);
+            }
+            cur[e] += excl;
+            tot[e] = excl;
+            if (e % nblk == (int)blk)
+                for (int64_t r = excl + cnt; r < excl + padded && r < a.reorder_cap; ++r) a.reorder[r] = -1;
+        }
+        base += __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+    if (blk == 0 && lane == 0) {
+        a.seg_indptr[L] = base;
+        if ((int64_t)base > a.reorder_cap) set_status(a.status, CDL_STATUS_REORDER_OVERFLOW);
+    }
+    // stable ranks, 64 slots a round
+#pragma unroll
+    for (int r = 0; r < TPB; ++r) {
+        const int i = begin + r * kWave + lane;
+        if (begin + r * kWave >= end) break;
+        const int32_t e = i < end ? local_expert(my[r], a.expert_begin, L) : -1;
+        uint64_t pending = __ballot(e >= 0);
+        int32_t dst = -1;
+        while (pending) {
+            const int leader = __builtin_ctzll(pending);
+            const int32_t el = __builtin_amdgcn_readlane(e, leader);
+            const uint64_t m = __ballot(e == el);
+            const int32_t before = cur[el];
+            if (e == el) dst = before + __popcll(m & lanes_below(lane));
+            if (lane == leader) cur[el] = before + __popcll(m);
+            pending &= ~m;
+        }
+        if (i < end) {
+            a.src2dst[i] = dst;
+            if (dst >= 0 && (int64_t)dst < a.reorder_cap) a.reorder[dst] = e;
+            dsts[r * kWave + lane] = dst;
+        }
+    }
+}
+
+// Layout and scatter in one launch (two with superblock counts): TPB row waves
+// quantise their tokens' rows while one more wave derives the workgroup's
+// destinations; after the one barrier the row waves store.  SELF: a small
+// batch, whose layout wave counts every slot itself, and whose rows are loaded
+// without first looking for a local slot.
+template <int TPB, bool SELF, bool LL>
+__global__ __launch_bounds__((TPB + 1) * kWave) void mx_permute_kernel(PermuteArgs a, const uint16_t *__restrict__ x,
+                                                                      int64_t H, uint8_t *__restrict__ oq,
+                                                                      uint8_t *__restrict__ os)
+{
+    static_assert(SELF || !LL, "the padded form of a large batch scatters from a given layout");
+    extern __shared__ int32_t lds[];
+    const int L = a.L, k = a.k, lane = threadIdx.x & (kWave - 1), wave = wave_id();
+    int32_t *tot = lds, *cur = lds + L, *dsts = lds + 2 * L;
+    const int64_t t = (int64_t)blockIdx.x * TPB + wave;
+    const bool real = wave < TPB && t < a.T;
+    int32_t id = 0;
+    bool row = false;
+    MxRow held;
+    if (wave == TPB) {
+        if constexpr (SELF)
+            mx_layout_self<TPB>(a, blockIdx.x, tot, cur, dsts);
+        else
+            layout_one_wave<TPB>(a, blockIdx.x, tot, cur, dsts);
+    } else if (real) {
+        const rsrc_t r_tok = make_rsrc(a.ids + t * k, (uint32_t)k * 4u);
+        id = buf_ld4(r_tok, (uint32_t)lane * 4u, 0);
+        row = SELF || __ballot(lane < k && local_expert(id, a.expert_begin, L) >= 0) != 0;
+        if (row) held.load_quant(make_rsrc(x + t * H, (uint32_t)(H * 2)), lane, 0);
+    }
+    __syncthreads();
+    if (!row) return;
+    int32_t d = lane < k ? dsts[wave * k + lane] : -1;
+    bool drop = false;
+    if constexpr (LL) {
+        const int32_t e = d >= 0 ? local_expert(id, a.expert_begin, L) : 0;
+        const int64_t slot = d >= 0 ? d - tot[e] : 0;
+        drop = d >= 0 && slot >= a.ll_cap;
+        d = d < 0 || drop ? -1 : (int32_t)(e * a.ll_cap + slot);
+        if (lane < k) a.ll_src2dst[t * k + lane] = d;
+        if (__ballot(drop) != 0 && lane == 0) set_status(a.status, CDL_STATUS_LL_OVERFLOW);
+    } else {
+        drop = d >= 0 && (int64_t)d >= a.cap_rows;
+        if (__ballot(drop) != 0 && lane == 0) set_status(a.status, CDL_STATUS_ROWS_OVERFLOW);
+        if (drop) d = -1;
+    }
+    mx_store_token(x, t, H, lane, oq, os, d, __ballot(d >= 0), kMxPairs * 1024, &held);
 }
 
 // ---------------------------------------------------------------------------
@@ -996,8 +1169,6 @@ struct FewColumns {
     }
 };
 
-__device__ __forceinline__ uint64_t lanes_below(int lane) { return lane ? ~0ull >> (kWave - lane) : 0ull; }
-
 // First kernel: h[slot, i] = silu(gate) * up for 16 columns i of the a-th
 // listed expert (blockIdx.y); blockIdx.x is the column tile.  The 4 waves take
 // the turns of the depth in rotation, a part of a turn being multiplied while
@@ -1425,6 +1596,49 @@ int launch_mx_scatter(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
     return launch_status();
 }
 
+// Small batches (T * k <= 4096) lay themselves out in the launch that moves
+// their rows; one token a workgroup while there are few.
+constexpr int64_t kMxSelfSlots = 4096;
+
+template <bool LL>
+int launch_mx_permute_self(const PermuteArgs &a, const uint16_t *x, int64_t H, uint8_t *q, uint8_t *s,
+                           hipStream_t stream)
+{
+    const int tpb = a.T <= 512 ? 1 : 4;
+    const size_t lds = (size_t)(2 * a.L + tpb * a.k) * sizeof(int32_t);
+    const dim3 grid((unsigned)((a.T + tpb - 1) / tpb));
+    if (tpb == 1)
+        mx_permute_kernel<1, true, LL><<<grid, dim3(2 * kWave), lds, stream>>>(a, x, H, q, s);
+    else
+        mx_permute_kernel<4, true, LL><<<grid, dim3(5 * kWave), lds, stream>>>(a, x, H, q, s);
+    return launch_status();
+}
+
+// Larger ones count their superblocks first.
+int launch_mx_permute(PermuteArgs a, const uint16_t *x, int64_t H, uint8_t *q, uint8_t *s, void *ws,
+                      hipStream_t stream)
+{
+    const Plan p = make_plan(a.T, a.k, a.L, kMaxTpbFp8);
+    a.sb_counts = (const int32_t *)ws;
+    a.S = p.S;
+    a.sbb_shift = 0;
+    while ((int64_t)1 << a.sbb_shift < p.sbb) ++a.sbb_shift;     // sbb is a power of two
+    a.sb_slots = p.sb_slots;
+    if (p.S * (int64_t)a.L > (int64_t)INT32_MAX) return CDL_ERR_TOO_LARGE;
+    layout_count_kernel<<<dim3((unsigned)p.S), dim3(kCountThreads), a.L * sizeof(int32_t), stream>>>(
+        a.ids, p.n, p.sb_slots, a.expert_begin, a.L, (int32_t *)ws);
+    int rc = launch_status();
+    if (rc != CDL_OK) return rc;
+    const size_t lds = (size_t)(2 * a.L + p.tpb * a.k) * sizeof(int32_t);
+    const dim3 grid((unsigned)p.nblocks);
+    switch (p.tpb) {
+    case 1: mx_permute_kernel<1, false, false><<<grid, dim3(2 * kWave), lds, stream>>>(a, x, H, q, s); break;
+    case 2: mx_permute_kernel<2, false, false><<<grid, dim3(3 * kWave), lds, stream>>>(a, x, H, q, s); break;
+    default: mx_permute_kernel<4, false, false><<<grid, dim3(5 * kWave), lds, stream>>>(a, x, H, q, s); break;
+    }
+    return launch_status();
+}
+
 int check_grouped(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t K, const uint8_t *wq,
                   const uint8_t *ws, int32_t L, int64_t N, const int32_t *counts, const int64_t *seg, int64_t cap)
 {
@@ -1594,10 +1808,10 @@ int cdl_dequant_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int
     if (!q || !scales || !out) return CDL_ERR_NULL_POINTER;
     if (!aligned(q, 8) || !aligned(out, 16)) return CDL_ERR_UNSUPPORTED;
     if (rows > INT64_MAX / 2 / H) return CDL_ERR_TOO_LARGE;
-    const int64_t n16 = rows * (H / 16);
-    const int64_t blocks = (n16 + 255) / 256;
+    const int64_t n8 = rows * (H / 8);
+    const int64_t blocks = (n8 + 256 * kMxDequantSteps - 1) / (256 * kMxDequantSteps);
     mx_dequant_kernel<<<dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, (hipStream_t)stream>>>(
-        (const u32x2 *)q, scales, n16, (u32x4 *)out);
+        (const uint32_t *)q, scales, n8, (u32x4 *)out);
     return launch_status();
 }
 
@@ -1635,10 +1849,10 @@ int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
     if (!aligned(x, 16) || !aligned(out_q, 8)) return CDL_ERR_UNSUPPORTED;
     PermuteArgs a = layout_args(topk_ids, T, k, expert_begin, L, alignment, counts, seg_indptr, src2dst,
                                 reorder_topk_ids, reorder_cap, status);
-    rc = run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
-    if (rc != CDL_OK) return rc;
-    return launch_mx_scatter<false>(x, T, H, k, src2dst, out_q, out_scales, cap_rows, status, MxLL{},
-                                    (hipStream_t)stream);
+    a.cap_rows = cap_rows;
+    if (T == 0) return run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
+    if (T * k <= kMxSelfSlots) return launch_mx_permute_self<false>(a, x, H, out_q, out_scales, (hipStream_t)stream);
+    return launch_mx_permute(a, x, H, out_q, out_scales, ws, (hipStream_t)stream);
 }
 
 int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,
@@ -1659,6 +1873,12 @@ int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, con
     if (!aligned(x, 16) || !aligned(out_q, 8)) return CDL_ERR_UNSUPPORTED;
     PermuteArgs a = layout_args(topk_ids, T, k, expert_begin, L, 1, counts, seg_indptr, src2dst, reorder_topk_ids,
                                 reorder_cap, status);
+    if (T > 0 && T * k <= kMxSelfSlots) {
+        a.ll_cap = cap;
+        a.masked_m = masked_m;
+        a.ll_src2dst = ll_src2dst;
+        return launch_mx_permute_self<true>(a, x, H, out_q, out_scales, (hipStream_t)stream);
+    }
     rc = run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
     if (rc != CDL_OK) return rc;
     const MxLL ll = {topk_ids, expert_begin, L, seg_indptr, counts, cap, masked_m, ll_src2dst};
