@@ -21,6 +21,14 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+// Two fp32 values to a pair of bf16, round to nearest even: one
+// v_cvt_pk_bf16_f32 (any NaN stays one; the dispatch's own conversion also
+// fixes its pattern, at several instructions a value).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, v2bf16{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
+
 // The scale byte of a group from the bits of its largest magnitude as a
 // bf16 (16 bits): the smallest power of two 2^(b - 127), b >= 0, with
 // 6 * 2^(b - 127) >= amax.  amax = 1.f * 2^(E - 127) and 6 = 1.5 * 2^2, so
@@ -538,33 +546,72 @@ __device__ __forceinline__ void store_swiglu_group(const float (&h)[16], int lan
     if (lane < 32) *s = nan ? (uint8_t)255 : (uint8_t)b;
 }
 
-// A 32 x 32 block of products to bf16 rows: lane l has token column l % 32 and
-// weight rows 8 b + 4 (l / 32) + i in v[4 b + i].  The two lanes of a column
-// trade quads, so that each holds 8 consecutive columns of the row (one
-// 16-byte store) per 16.
-__device__ __forceinline__ void store_rows_bf16(const f32x16 &v, int lane, bool live, uint16_t *row, int n, int live_n,
-                                                int64_t N)
+// Exchanges that transpose a quad's 4 x 4 words: lane q's v[j] becomes lane
+// j's v[q].
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_word(uint32_t v)
 {
-    const int half = lane >> 5;
-    uint32_t p[8];
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ void transpose_quad(int lane, uint32_t &v0, uint32_t &v1, uint32_t &v2, uint32_t &v3)
+{
+    constexpr int kXor1 = 0xB1, kXor2 = 0x4E;          // quad_perm [1,0,3,2], [2,3,0,1]
+    const bool odd = lane & 1, high = lane & 2;
+    // (every exchange is made by all lanes, the selects follow)
+    const uint32_t x0 = dpp_word<kXor1>(v0), x1 = dpp_word<kXor1>(v1);
+    const uint32_t x2 = dpp_word<kXor1>(v2), x3 = dpp_word<kXor1>(v3);
+    const uint32_t a0 = odd ? x1 : v0, a1 = odd ? v1 : x0, a2 = odd ? x3 : v2, a3 = odd ? v3 : x2;
+    const uint32_t y0 = dpp_word<kXor2>(a0), y1 = dpp_word<kXor2>(a1);
+    const uint32_t y2 = dpp_word<kXor2>(a2), y3 = dpp_word<kXor2>(a3);
+    v0 = high ? y2 : a0;
+    v1 = high ? y3 : a1;
+    v2 = high ? a2 : y0;
+    v3 = high ? a3 : y1;
+}
+
+// Two 32 x 32 blocks of products to bf16 rows: lane l has token column l % 32
+// of both, weight rows 8 b + 4 (l / 32) + i in [4 b + i].  The halves trade so
+// that the lower lanes have block x's 32 columns of their row and the upper
+// ones block y's, 4 chunks of 16 bytes; then the lanes of a quad trade so that
+// each store writes runs of 64 bytes (one lane's 16 bytes of a row are a
+// request of their own otherwise: 131072 rows of 128 experts, K = N = 4096,
+// 1307 -> 1180 us).
+//   to    the lane's block: its first of 32 rows, at its first column
+//   rows, cols  rows and columns of the block that are written
+__device__ __forceinline__ void store_blocks_bf16(const f32x16 &x, const f32x16 &y, int lane, uint16_t *to, int rows,
+                                                  int cols, int64_t N, bool vector)
+{
+    uint32_t p[8], q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = pack_bf16_rne(v[2 * i], v[2 * i + 1]);
-    if (N % 8 == 0 && ((uintptr_t)row & 15) == 0) {        // rows keep the 16-byte alignment
+    for (int i = 0; i < 8; ++i) {
+        p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        q[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
+        swap_halves(p[i], q[i]);
+    }
+    u32x4 v[4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            // p[4b], p[4b+1]: columns 16 b + 4 half + 0..3; p[4b+2], p[4b+3]: 8 more
-            swap_halves(p[4 * b], p[4 * b + 2]);
-            swap_halves(p[4 * b + 1], p[4 * b + 3]);
-            const u32x4 w = {p[4 * b], p[4 * b + 1], p[4 * b + 2], p[4 * b + 3]};
-            const int c = n + 16 * b + 8 * half;
-            if (live && c < live_n) *reinterpret_cast<u32x4 *>(row + c) = w;
+    for (int b = 0; b < 4; ++b) v[b] = u32x4{p[2 * b], p[2 * b + 1], q[2 * b], q[2 * b + 1]};
+    const int r = lane & 31;
+    if (vector) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t t[4] = {v[0][w], v[1][w], v[2][w], v[3][w]};
+            transpose_quad(lane, t[0], t[1], t[2], t[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j][w] = t[j];
         }
-    } else if (live) {
+        const int c = (lane & 3) * 8, r0 = r & ~3;
+        uint16_t *o = to + r0 * N + c;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int c = n + 8 * (i / 4) + 4 * half + i % 4;
-            if (c < live_n) row[c] = (uint16_t)(p[i / 2] >> (16 * (i & 1)));
-        }
+        for (int j = 0; j < 4; ++j, o += N)
+            if (r0 + j < rows && c < cols) *reinterpret_cast<u32x4 *>(o) = v[j];
+    } else if (r < rows) {
+        uint16_t *o = to + r * N;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * b + e < cols) o[8 * b + e] = (uint16_t)(v[b][e / 2] >> (16 * (e & 1)));
     }
 }
 
@@ -912,14 +959,13 @@ struct GroupedWg {
     __device__ __forceinline__ void store_tile(int64_t row_first, int64_t n_first, int rows_m, int cols)
     {
         const int wn = wave % S::WN, wm = wave / S::WN;
+        if constexpr (SWIGLU) {
+            constexpr int H = S::NF / 2;
+            const int64_t I = a.N / 2;
 #pragma unroll
-        for (int j = 0; j < S::MF; ++j) {
-            const int m = (wm * S::MF + j) * 32 + (lane & 31);
-            const bool live = m < rows_m;
-            const int64_t row = row_first + m;
-            if constexpr (SWIGLU) {
-                constexpr int H = S::NF / 2;
-                const int64_t I = a.N / 2;
+            for (int j = 0; j < S::MF; ++j) {
+                const int m = (wm * S::MF + j) * 32 + (lane & 31);
+                const int64_t row = row_first + m;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     const int n = (wn * H + i) * 32;
@@ -927,15 +973,24 @@ struct GroupedWg {
                     float h[16];
 #pragma unroll
                     for (int v = 0; v < 16; ++v) h[v] = acc[i][j][v] / (1.0f + __expf(-acc[i][j][v])) * acc[i + H][j][v];
-                    store_swiglu_group(h, lane, live, a.hq + row * (I / 2) + (n_first + n) / 2,
+                    store_swiglu_group(h, lane, m < rows_m, a.hq + row * (I / 2) + (n_first + n) / 2,
                                        a.hs + row * (I / 32) + (n_first + n) / 32);
                 }
-            } else {
+            }
+        } else {
+            const bool vector = a.N % 8 == 0 && ((uintptr_t)a.out & 15) == 0;      // rows keep the 16-byte alignment
+            // pairs of blocks: both token fragments of a weight fragment, or
+            // (one token fragment) two weight fragments
+            constexpr int P = S::MF == 2 ? S::NF : S::NF / 2;
+            static_assert(S::MF == 2 || S::MF == 1, "token fragments per wave");
 #pragma unroll
-                for (int i = 0; i < S::NF; ++i) {
-                    store_rows_bf16(acc[i][j], lane, live, a.out + row * a.N + n_first, (wn * S::NF + i) * 32, cols, a.N);
-                    __builtin_amdgcn_sched_barrier(0);     // one block's temporaries at a time
-                }
+            for (int i = 0; i < P; ++i) {
+                const int up = lane >> 5;
+                const int n = (wn * S::NF + (S::MF == 2 ? i : 2 * i + up)) * 32;
+                const int m = (wm * S::MF + (S::MF == 2 ? up : 0)) * 32;
+                store_blocks_bf16(acc[S::MF == 2 ? i : 2 * i][0], S::MF == 2 ? acc[i][1 % S::MF] : acc[(2 * i + 1) % S::NF][0],
+                                  lane, a.out + (row_first + m) * a.N + n_first + n, rows_m - m, cols - n, a.N, vector);
+                __builtin_amdgcn_sched_barrier(0);     // one pair's temporaries at a time
             }
         }
     }
@@ -1371,7 +1426,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i];
                 *reinterpret_cast<u32x2 *>(a.h + (int64_t)slot * a.I + i0 + 4 * g) =
-                    u32x2{pack_bf16_rne(h[0], h[1]), pack_bf16_rne(h[2], h[3])};
+                    u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
             }
         }
     }
@@ -1559,7 +1614,7 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             s0 += sums[((size_t)w * a.T + t) * 16 + j];
             s1 += sums[((size_t)w * a.T + t) * 16 + j + 1];
         }
-        if (j < rows_n) *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.H + n0 + j) = pack_bf16_rne(s0, s1);
+        if (j < rows_n) *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.H + n0 + j) = pack_bf16(s0, s1);
     }
 }
 
