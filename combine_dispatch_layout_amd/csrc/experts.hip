@@ -575,7 +575,7 @@ __device__ __forceinline__ void transpose_quad(int lane, uint32_t &v0, uint32_t 
 // ones block y's, 4 chunks of 16 bytes; then the lanes of a quad trade so that
 // each store writes runs of 64 bytes (one lane's 16 bytes of a row are a
 // request of their own otherwise: 131072 rows of 128 experts, K = N = 4096,
-// 1307 -> 1180 us).
+// 1307 -> 1274 us).
 //   to    the lane's block: its first of 32 rows, at its first column
 //   rows, cols  rows and columns of the block that are written
 __device__ __forceinline__ void store_blocks_bf16(const f32x16 &x, const f32x16 &y, int lane, uint16_t *to, int rows,
@@ -655,18 +655,24 @@ struct GroupedShape {
     static constexpr int MF = MT / 32 / WM;
     static constexpr int kRows = kGroupedNT + MT;        // LDS rows of a stage
     static constexpr int kUnits = kRows * 8 / kGroupedThreads;   // 16-byte units per thread and stage
-    // codes of two stages, their scales (8 bytes a row, a row per thread), then the tile table
-    static constexpr size_t kLds = 2 * (size_t)kRows * kStage + 2 * (size_t)kGroupedThreads * 8;
+    // codes of two stages, the scales of two pairs of stages (16 bytes a row, a row per thread), then the tile table
+    static constexpr size_t kLds = 2 * (size_t)kRows * kStage + 2 * (size_t)kGroupedThreads * 16;
 };
 
-// A stage's 8 scale bytes of a row that start at byte `at` of the descriptor,
-// from the three aligned words that hold them; bytes from `left` on are zero.
-typedef unsigned int u32x3 __attribute__((ext_vector_type(3)));
-__device__ __forceinline__ u32x2 stage_scale_bytes(u32x3 v, uint32_t at, int left)
+// The 16 scale bytes of two stages of a row that start at byte `at` of the
+// descriptor, from the aligned words that hold them; bytes from `left` on are
+// zero.
+__device__ __forceinline__ u32x4 pair_scale_bytes(u32x4 v, uint32_t x, uint32_t at, int left)
 {
-    const uint64_t keep = left >= 8 ? ~0ull : left <= 0 ? 0ull : ~0ull >> (64 - 8 * left);
-    return u32x2{__builtin_amdgcn_alignbyte(v.y, v.x, at & 3u) & (uint32_t)keep,
-                 __builtin_amdgcn_alignbyte(v.z, v.y, at & 3u) & (uint32_t)(keep >> 32)};
+    const uint32_t w[5] = {v.x, v.y, v.z, v.w, x};
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = left - 4 * i;
+        const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : ~0u >> (32 - 8 * n);
+        o[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], at & 3u) & keep;
+    }
+    return o;
 }
 
 template <int MT, bool SWIGLU>
@@ -688,6 +694,7 @@ struct GroupedWg {
     const int tid, lane, wave;
     const uint32_t K2;
     const int K32;
+    const bool ragged;                       // scale rows not word-aligned
     const uint32_t unit_off, unit_lds;       // a thread's unit 0: operand offset, LDS offset
     const uint32_t scale_lds, scale_lane;    // its scale row's LDS offset; a lane's scale word in a fragment's
     const uint32_t frag_w, frag_b;           // a lane's first fragments: LDS offset at step 0
@@ -699,7 +706,9 @@ struct GroupedWg {
     uint32_t scale_off, sc_off;              // a thread's scale row; that of the scales in registers
     // registers on the way to LDS
     u32x4 stage[S::kUnits];
-    u32x3 sc;
+    u32x4 sc;
+    uint32_t sc_x;
+    int pair;                                // LDS buffer of the scales stored last
     // A weight fragment is read again for the next step as soon as the last
     // instruction that takes it is issued; the token fragments, which every
     // instruction of a step takes, alternate between two sets.
@@ -720,10 +729,11 @@ struct GroupedWg {
     __device__ __forceinline__ GroupedWg(const GroupedArgs &args, uint8_t *l)
         : a(args), lds(l), tid(threadIdx.x), lane(tid & (kWave - 1)), wave(wave_id()), K2((uint32_t)(args.K / 2)),
           K32((int)(args.K / 32)),
+          ragged((((uint32_t)K32 | (uint32_t)(uintptr_t)args.s | (uint32_t)(uintptr_t)args.ws) & 3u) != 0),
           unit_off((uint32_t)(tid >> 3) % 32 * K2 + (uint32_t)(tid & 7) * 16),
           unit_lds((uint32_t)(tid >> 3) * kStage + (uint32_t)(((tid & 7) ^ (tid >> 4 & 7)) << 4)),
-          scale_lds(2 * kBuf + scale_row(tid) * 8),
-          scale_lane((uint32_t)((lane & 31) * 8 + (lane >> 5) * 4)),
+          scale_lds(2 * kBuf + scale_row(tid) * 16),
+          scale_lane((uint32_t)((lane & 31) * 16 + (lane >> 5) * 4)),
           frag_w((uint32_t)((wave % S::WN) * S::NF * 32 + (lane & 31)) * kStage +
                  (uint32_t)(((4 * (lane >> 5)) ^ (lane >> 1 & 7)) << 4)),
           frag_b((uint32_t)(kGroupedNT + (wave / S::WN) * S::MF * 32 + (lane & 31)) * kStage +
@@ -799,18 +809,23 @@ struct GroupedWg {
     {
         *reinterpret_cast<u32x4 *>(lds + (unit_lds + (uint32_t)(buf * kBuf)) + j * (64 * kStage)) = stage[j];
     }
-    // the scales of stage s, one row a thread (threads past the rows: zeros)
+    // The scales of stages s and s + 1 (s even), one row a thread (threads past
+    // the rows: zeros): every row is a cache line of its own, so that a load
+    // for each stage costs as much as the codes' (decode 95 -> 86 us, 4096
+    // rows of 32 experts 135 -> 126 us by taking two stages at once).
     __device__ __forceinline__ void load_scales(int s)
     {
-        const uint32_t at = scale_off + 8u * (uint32_t)s;
+        const rsrc_t r = make_rsrc(scale_ptr, scale_bytes);
+        const uint32_t at = (scale_off + 8u * (uint32_t)s) & ~3u;
         sc_off = scale_off;
-        sc = __builtin_amdgcn_raw_buffer_load_b96(make_rsrc(scale_ptr, scale_bytes), at & ~3u, 0, 0);
+        sc = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+        sc_x = ragged ? (uint32_t)buf_ld4(r, at + 16u, 0) : 0u;
     }
-    // into LDS buffer buf, as the scales of stage s of their tile
-    __device__ __forceinline__ void store_scales(int buf, int s)
+    __device__ __forceinline__ void store_scales(int s)
     {
-        *reinterpret_cast<u32x2 *>(lds + scale_lds + buf * (kGroupedThreads * 8)) =
-            stage_scale_bytes(sc, sc_off, K32 - 8 * s);
+        pair ^= 1;
+        *reinterpret_cast<u32x4 *>(lds + scale_lds + pair * (kGroupedThreads * 16)) =
+            pair_scale_bytes(sc, sc_x, sc_off, K32 - 8 * s);
     }
 
     // fragments of step `st` of the stage in LDS buffer buf
@@ -824,16 +839,19 @@ struct GroupedWg {
         return *reinterpret_cast<const u32x4 *>(lds + ((frag_b ^ (uint32_t)(st << 4)) + (uint32_t)(buf * kBuf)) +
                                                 m * (32 * kStage));
     }
-    // scale words of the stage in LDS buffer buf
-    __device__ __forceinline__ int weight_scale(int buf, int n) const
+    // scale words of stage s of a tile, whose pair was stored last
+    __device__ __forceinline__ uint32_t pair_scales(int s) const
     {
-        return *reinterpret_cast<const int *>(lds + (2 * kBuf + (uint32_t)(buf * (kGroupedThreads * 8)) + scale_lane) +
-                                              wave % S::WN * (S::NF * 256) + n * 256);
+        return 2 * kBuf + (uint32_t)(pair * (kGroupedThreads * 16) + (s & 1) * 8) + scale_lane;
     }
-    __device__ __forceinline__ int token_scale(int buf, int m) const
+    __device__ __forceinline__ int weight_scale(int s, int n) const
     {
-        return *reinterpret_cast<const int *>(lds + (2 * kBuf + (uint32_t)(buf * (kGroupedThreads * 8)) + scale_lane) +
-                                              wave / S::WN * (S::MF * 256) + (kGroupedNT / 32 + m) * 256);
+        return *reinterpret_cast<const int *>(lds + pair_scales(s) + wave % S::WN * (S::NF * 512) + n * 512);
+    }
+    __device__ __forceinline__ int token_scale(int s, int m) const
+    {
+        return *reinterpret_cast<const int *>(lds + pair_scales(s) + wave / S::WN * (S::MF * 512) +
+                                              (kGroupedNT / 32 + m) * 512);
     }
 
     // Share of `total` items that follows matrix instruction i of `of`.
@@ -846,9 +864,10 @@ struct GroupedWg {
     }
 
     // Step ST of the stage in LDS buffer buf: its matrix instructions, each
-    // followed by the reads for the next step and by work(i).
+    // followed by the reads for the next step (after the last, of stage `next`
+    // of its tile) and by work(i).
     template <int ST, typename F>
-    __device__ __forceinline__ void multiply(int buf, F &&work)
+    __device__ __forceinline__ void multiply(int buf, int next, F &&work)
     {
         constexpr int NM = S::NF * S::MF, SET = ST & 1, nst = (ST + 1) & 3;
         const int nbuf = ST == 3 ? buf ^ 1 : buf;
@@ -860,11 +879,11 @@ struct GroupedWg {
             __builtin_amdgcn_sched_barrier(0);
             share(i, NM, S::MF, [&](int x) {
                 fb[SET ^ 1][x] = token_fragment(nbuf, nst, x);
-                if (ST == 3) sb_next[x] = token_scale(nbuf, x);
+                if (ST == 3) sb_next[x] = token_scale(next, x);
             });
             if (m == S::MF - 1) {
                 fw[n] = weight_fragment(nbuf, nst, n);
-                if (ST == 3) sw[n] = weight_scale(nbuf, n);
+                if (ST == 3) sw[n] = weight_scale(next, n);
             }
             work(i);
             __builtin_amdgcn_sched_barrier(0);
@@ -885,24 +904,20 @@ struct GroupedWg {
             store_unit(buf ^ 1, x);
             load_unit(&off, off0, x);
         };
-        auto scales = [&] {
-            store_scales(buf ^ 1, held);
-            load_scales(load);
-        };
+        if (!(held & 1)) store_scales(held);
+        if (!(load & 1)) load_scales(load);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (BUSY) {
-            multiply<0>(buf, [&](int i) { share(i, 2 * NM, U, refill); });
-            multiply<1>(buf, [&](int i) { share(i + NM, 2 * NM, U, refill); });
-            multiply<2>(buf, [&](int i) {
-                if (i == 0) scales();
-            });
+            multiply<0>(buf, held, [&](int i) { share(i, 2 * NM, U, refill); });
+            multiply<1>(buf, held, [&](int i) { share(i + NM, 2 * NM, U, refill); });
+            multiply<2>(buf, held, [&](int) {});
             __syncthreads();
-            multiply<3>(buf, [&](int) {});
+            multiply<3>(buf, held, [&](int) {});
 #pragma unroll
             for (int j = 0; j < S::MF; ++j) sb[j] = sb_next[j];
         } else {
 #pragma unroll
             for (int x = 0; x < U; ++x) refill(x);
-            scales();
             __syncthreads();
         }
     }
@@ -922,8 +937,8 @@ struct GroupedWg {
             store_unit(0, j);
             load_unit(&off, off0, j);
         }
-        store_scales(0, 0);
-        load_scales(1);
+        pair = 1;
+        store_scales(0);
         __syncthreads();
     }
 
@@ -936,14 +951,14 @@ struct GroupedWg {
         if constexpr (BUSY) {
 #pragma unroll
             for (int i = 0; i < S::NF; ++i) {
-                sw[i] = weight_scale(buf, i);
+                sw[i] = weight_scale(0, i);
                 fw[i] = weight_fragment(buf, 0, i);
 #pragma unroll
                 for (int j = 0; j < S::MF; ++j) acc[i][j] = f32x16{};
             }
 #pragma unroll
             for (int j = 0; j < S::MF; ++j) {
-                sb[j] = token_scale(buf, j);
+                sb[j] = token_scale(0, j);
                 fb[0][j] = token_fragment(buf, 0, j);
             }
         }
