@@ -731,6 +731,18 @@ def ll_expected_m(T: int, num_ranks: int, k: int, num_experts: int) -> int:
 # MXFP4 rows, the grouped product, and the layer of a few tokens
 # ---------------------------------------------------------------------------
 
+def _launch(what: str, dev: torch.device, *args) -> None:
+    """One call of the C ABI on the device's current stream, with that device
+    current (the tensors' device need not be the caller's current one)."""
+    fn = getattr(library(), what)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    _check(rc, what)
+
+
 def _mx_width(H: int, what: str) -> None:
     if H < 1 or H % MXFP4_GROUP:
         raise CdlError(-3, "%s (row length must be a multiple of %d)" % (what, MXFP4_GROUP))
@@ -771,8 +783,7 @@ def quant_mxfp4(x: torch.Tensor, out_q: Optional[torch.Tensor] = None,
     _mx_width(H, "quant_mxfp4")
     out_q, out_scales = _mx_out(out_q, out_scales, x.shape[:-1], H, x.device)
     _same_device(x.device, out_q=out_q, out_scales=out_scales)
-    rc = library().cdl_quant_mxfp4(_ptr(x), x.numel() // H, H, _ptr(out_q), _ptr(out_scales), _stream(x.device))
-    _check(rc, "cdl_quant_mxfp4")
+    _launch("cdl_quant_mxfp4", x.device, _ptr(x), x.numel() // H, H, _ptr(out_q), _ptr(out_scales))
     return out_q, out_scales
 
 
@@ -783,8 +794,7 @@ def dequant_mxfp4(q: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Ten
         out = torch.empty(*q.shape[:-1], H, dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, (*q.shape[:-1], H))
     _same_device(q.device, scales=scales, out=out)
-    rc = library().cdl_dequant_mxfp4(_ptr(q), _ptr(scales), out.numel() // H, H, _ptr(out), _stream(q.device))
-    _check(rc, "cdl_dequant_mxfp4")
+    _launch("cdl_dequant_mxfp4", q.device, _ptr(q), _ptr(scales), out.numel() // H, H, _ptr(out))
     return out
 
 
@@ -819,9 +829,8 @@ def dispatch_mxfp4(x: torch.Tensor, layout: Layout, out_q: Optional[torch.Tensor
     if status is not None:
         _need(status, "status", torch.int32)
     _same_device(x.device, src2dst=layout.src2dst, out_q=out_q, out_scales=out_scales, status=status)
-    rc = library().cdl_dispatch_mxfp4(_ptr(x), T, H, k, _ptr(layout.src2dst), _ptr(out_q), _ptr(out_scales),
-                                      out_q.shape[0], _ptr(status), _stream(x.device))
-    _check(rc, "cdl_dispatch_mxfp4")
+    _launch("cdl_dispatch_mxfp4", x.device, _ptr(x), T, H, k, _ptr(layout.src2dst), _ptr(out_q),
+            _ptr(out_scales), out_q.shape[0], _ptr(status))
     return out_q, out_scales
 
 
@@ -840,12 +849,10 @@ def permute_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, expert_begin: int, nu
         _need(status, "status", torch.int32)
     _same_device(x.device, topk_ids=lay.topk_ids, out_q=out_q, out_scales=out_scales, status=status,
                  workspace=ws)
-    rc = library().cdl_permute_mxfp4(_ptr(x), T, H, k, _ptr(lay.topk_ids), lay.expert_begin, L, lay.alignment,
-                                     _ptr(lay.counts), _ptr(lay.seg_indptr), _ptr(lay.src2dst),
-                                     _ptr(lay.reorder_buf), lay.reorder_buf.numel(), _ptr(out_q),
-                                     _ptr(out_scales), out_q.shape[0], _ptr(status), _ptr(ws),
-                                     ws.numel() * ws.element_size(), _stream(x.device))
-    _check(rc, "cdl_permute_mxfp4")
+    _launch("cdl_permute_mxfp4", x.device, _ptr(x), T, H, k, _ptr(lay.topk_ids), lay.expert_begin, L,
+            lay.alignment, _ptr(lay.counts), _ptr(lay.seg_indptr), _ptr(lay.src2dst), _ptr(lay.reorder_buf),
+            lay.reorder_buf.numel(), _ptr(out_q), _ptr(out_scales), out_q.shape[0], _ptr(status), _ptr(ws),
+            ws.numel() * ws.element_size())
     return lay, out_q, out_scales
 
 
@@ -865,12 +872,10 @@ def permute_ll_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, expert_begin: int,
         _need(status, "status", torch.int32)
     _same_device(x.device, topk_ids=lay.topk_ids, out_q=out_q, out_scales=out_scales, status=status,
                  workspace=ws)
-    rc = library().cdl_permute_ll_mxfp4(_ptr(x), T, H, k, _ptr(lay.topk_ids), lay.expert_begin, L,
-                                        _ptr(lay.counts), _ptr(lay.seg_indptr), _ptr(lay.src2dst),
-                                        _ptr(lay.reorder_buf), lay.reorder_buf.numel(), int(cap), _ptr(out_q),
-                                        _ptr(out_scales), _ptr(masked_m), _ptr(ll_map), _ptr(status), _ptr(ws),
-                                        ws.numel() * ws.element_size(), _stream(x.device))
-    _check(rc, "cdl_permute_ll_mxfp4")
+    _launch("cdl_permute_ll_mxfp4", x.device, _ptr(x), T, H, k, _ptr(lay.topk_ids), lay.expert_begin, L,
+            _ptr(lay.counts), _ptr(lay.seg_indptr), _ptr(lay.src2dst), _ptr(lay.reorder_buf),
+            lay.reorder_buf.numel(), int(cap), _ptr(out_q), _ptr(out_scales), _ptr(masked_m), _ptr(ll_map),
+            _ptr(status), _ptr(ws), ws.numel() * ws.element_size())
     return lay, out_q, out_scales, masked_m, ll_map
 
 
@@ -911,10 +916,8 @@ def grouped_mxfp4(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_sc
         out = torch.empty(*lead, N, dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, (*lead, N))
     _same_device(q.device, out=out)
-    rc = library().cdl_grouped_mxfp4(_ptr(q), _ptr(scales), lead.numel(), K, _ptr(w_q), _ptr(w_scales), L, N,
-                                     _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status),
-                                     _stream(q.device))
-    _check(rc, "cdl_grouped_mxfp4")
+    _launch("cdl_grouped_mxfp4", q.device, _ptr(q), _ptr(scales), lead.numel(), K, _ptr(w_q), _ptr(w_scales),
+            L, N, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status))
     return out
 
 
@@ -933,10 +936,9 @@ def grouped_swiglu_mxfp4(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tenso
     _mx_width(I, "grouped_swiglu_mxfp4")
     out_q, out_scales = _mx_out(out_q, out_scales, lead, I, q.device)
     _same_device(q.device, out_q=out_q, out_scales=out_scales)
-    rc = library().cdl_grouped_swiglu_mxfp4(_ptr(q), _ptr(scales), lead.numel(), K, _ptr(w_q), _ptr(w_scales), L,
-                                            I, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out_q),
-                                            _ptr(out_scales), _ptr(status), _stream(q.device))
-    _check(rc, "cdl_grouped_swiglu_mxfp4")
+    _launch("cdl_grouped_swiglu_mxfp4", q.device, _ptr(q), _ptr(scales), lead.numel(), K, _ptr(w_q),
+            _ptr(w_scales), L, I, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out_q), _ptr(out_scales),
+            _ptr(status))
     return out_q, out_scales
 
 
@@ -988,10 +990,8 @@ def moe_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tenso
         raise ValueError("w13 must be [L, 2 I, H] and w2 [L, H, I] with H = %d, got %s and %s"
                          % (H, tuple(w13.shape), tuple(w2.shape)))
     _same_device(x.device, w13=w13, w2=w2)
-    rc = library().cdl_moe_layer(_ptr(x), T, H, k, _ptr(ids), _ptr(topk_weights), int(expert_begin), L, I,
-                                 _ptr(w13), _ptr(w2), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
-                                 _stream(x.device))
-    _check(rc, "cdl_moe_layer")
+    _launch("cdl_moe_layer", x.device, _ptr(x), T, H, k, _ptr(ids), _ptr(topk_weights), int(expert_begin), L,
+            I, _ptr(w13), _ptr(w2), _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
     return out
 
 
@@ -1009,8 +1009,7 @@ def moe_layer_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
         raise ValueError("w13_q and w2_q must be [L, 2 I, H / 2] and [L, H, I / 2] with H = %d, got %s and %s"
                          % (H, tuple(w13_q.shape), tuple(w2_q.shape)))
     _same_device(x.device, w13_q=w13_q, w13_scales=w13_scales, w2_q=w2_q, w2_scales=w2_scales)
-    rc = library().cdl_moe_layer_mxfp4(_ptr(x), T, H, k, _ptr(ids), _ptr(topk_weights), int(expert_begin), L, I,
-                                       _ptr(w13_q), _ptr(w13_scales), _ptr(w2_q), _ptr(w2_scales), _ptr(out),
-                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(x.device))
-    _check(rc, "cdl_moe_layer_mxfp4")
+    _launch("cdl_moe_layer_mxfp4", x.device, _ptr(x), T, H, k, _ptr(ids), _ptr(topk_weights),
+            int(expert_begin), L, I, _ptr(w13_q), _ptr(w13_scales), _ptr(w2_q), _ptr(w2_scales), _ptr(out),
+            _ptr(ws), ws.numel() * ws.element_size())
     return out

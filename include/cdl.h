@@ -523,8 +523,9 @@ int cdl_dispatch_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const
                        void *stream);
 
 /*
- * cdl_permute_mxfp4 -- cdl_permute with MXFP4 rows: the layout, then the
- * scatter of cdl_dispatch_mxfp4.
+ * cdl_permute_mxfp4 -- cdl_permute with MXFP4 rows, those of
+ * cdl_dispatch_mxfp4.  One kernel launch for small batches (T*k <= 4096), two
+ * otherwise.
  */
 int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,
                       int32_t expert_begin, int32_t L, int32_t alignment, int32_t *counts,
@@ -561,7 +562,9 @@ int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
  *                      the buffer is cut to what does and sets
  *                      CDL_STATUS_ROWS_OVERFLOW (segments) or
  *                      CDL_STATUS_LL_OVERFLOW (padded)
- * K % 32 == 0, q and w_q 16-byte aligned; any N >= 1.
+ * K % 32 == 0, q and w_q 16-byte aligned; any N >= 1.  CDL_ERR_TOO_LARGE
+ * where L times the output tiles of one expert that owns the whole buffer (64
+ * rows, 256 columns) reaches 2^31.
  */
 int cdl_grouped_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t K,
                       const uint8_t *w_q, const uint8_t *w_scales, int32_t L, int64_t N,
@@ -607,7 +610,7 @@ size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
  *                     initialisation needed; calls that overlap need their own
  * T <= CDL_MOE_LAYER_MAX_TOKENS and T * k <= 4096 (CDL_ERR_UNSUPPORTED
  * otherwise: larger batches take the permute, the grouped products and the
- * combine); H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte aligned.  The
+ * combine); T * H and T * k * I below 2^31; H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte aligned.  The
  * sums are taken in a fixed order: the result is deterministic.
  */
 int cdl_moe_layer(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,

@@ -100,6 +100,8 @@ SCATTER = [  # T, H, E, L, k, begin, alignment, dist
     (64, 256, 8, 8, 2, 0, 1, "uniform"), (1, 32, 4, 4, 1, 0, 1, "uniform"), (3, 96, 16, 4, 3, 5, 16, "uniform"),
     (700, 2592, 32, 8, 8, 8, 1, "zipf"), (513, 7168, 64, 16, 6, 0, 128, "uniform"), (33, 7200, 8, 8, 4, 0, 1, "zipf"),
     (5000, 64, 128, 128, 8, 0, 1, "zipf"), (40, 128, 64, 2, 64, 3, 1, "uniform"),
+    (512, 64, 16, 16, 8, 0, 1, "uniform"), (513, 96, 16, 5, 7, 2, 32, "uniform"), (2048, 64, 4, 4, 2, 0, 1, "uniform"),
+    (4097, 32, 4, 3, 1, 0, 1, "zipf"), (64, 64, 2048, 2048, 64, 0, 1, "uniform"), (65, 64, 2048, 2048, 64, 0, 4, "uniform"),
 ]
 
 
@@ -150,7 +152,8 @@ def test_scatter_into_too_few_rows():
 
 
 @pytest.mark.parametrize("T,H,E,L,k,b,cap", [(128, 7168, 256, 32, 8, 0, 128), (64, 256, 8, 8, 2, 0, 9),
-                                             (600, 96, 16, 4, 3, 5, 700), (30, 64, 4, 4, 2, 0, 0)])
+                                             (600, 96, 16, 4, 3, 5, 700), (30, 64, 4, 4, 2, 0, 0),
+                                             (1500, 64, 16, 4, 3, 5, 1200), (1024, 7200, 8, 8, 4, 0, 300)])
 def test_permute_ll(T, H, E, L, k, b, cap):
     announce("mxfp4 low-latency T=%d H=%d L=%d cap=%d" % (T, H, L, cap))
     x, ids, _ = scatter_inputs(T, H, E, L, k, b, "uniform")
@@ -238,6 +241,55 @@ def test_grouped(counts, K, N, form):
         begins = seg
     assert int(st.item()) == 0
     check_grouped(a, sa, w, sw, counts, begins, out, canary)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("counts,K,N", [([70, 3], 1056, 260), ([300, 212], 736, 40), ([20, 90, 1], 2048, 513)])
+def test_grouped_scales_at_any_byte(counts, K, N, shift):
+    """Scale tensors that start at any byte, rows of an odd number of scales,
+    output rows at 2-byte alignment; the scales' neighbours are NaN codes."""
+    announce("grouped, scales at byte %d, counts=%s K=%d N=%d" % (shift, counts, K, N))
+    g = gen(shift + K)
+    L, rows = len(counts), sum(counts)
+
+    def moved(s):
+        flat = torch.full((s.numel() + 8,), 255, dtype=torch.uint8, device=DEV)
+        flat[shift:shift + s.numel()] = s.flatten()
+        return flat[shift:shift + s.numel()].view(s.shape)
+
+    w, sw = mx_random(g, L, N, K)
+    a, sa = mx_random(g, rows, K)
+    canary = torch.full((1,), -7.5, dtype=torch.bfloat16, device=DEV)
+    whole = canary.expand(rows * N + 16).contiguous()
+    out = whole[shift:shift + rows * N].view(rows, N)
+    seg = segments(counts)
+    cdl.grouped_mxfp4(a, moved(sa), w, moved(sw), torch.tensor(counts, dtype=torch.int32, device=DEV),
+                      torch.tensor(seg, device=DEV), out=out)
+    check_grouped(a, sa, w, sw, counts, seg, out, canary)
+    assert bool((whole[:shift] == -7.5).all()) and bool((whole[shift + rows * N:] == -7.5).all())
+    if N % 64 == 0 or N == 260:
+        I = N // 64 * 32
+        w2, sw2 = w[:, :2 * I].contiguous(), sw[:, :2 * I].contiguous()
+        q, s = cdl.grouped_swiglu_mxfp4(a, moved(sa), w2, moved(sw2),
+                                        torch.tensor(counts, dtype=torch.int32, device=DEV),
+                                        torch.tensor(seg, device=DEV))
+        for e, n in enumerate(counts):
+            at = slice(seg[e], seg[e] + n)
+            check_swiglu(a[at], sa[at], w2[e], sw2[e], q[at], s[at], I)
+
+
+@pytest.mark.parametrize("L,cap,n", [(128, 40, 7), (300, 3, 2), (2048, 2, 1)])
+def test_grouped_many_experts(L, cap, n):
+    """More experts than one scan of a wave takes; every third is empty."""
+    g = gen(L)
+    w, sw = mx_random(g, L, 24, 64)
+    a, sa = mx_random(g, L, cap, 64)
+    counts = [0 if e % 3 == 1 else n for e in range(L)]
+    canary = torch.full((1,), -7.5, dtype=torch.bfloat16, device=DEV)
+    out = canary.expand(L, cap, 24).contiguous()
+    cdl.grouped_mxfp4(a, sa, w, sw, torch.tensor(counts, dtype=torch.int32, device=DEV), out=out)
+    check_grouped(a.view(L * cap, -1), sa.view(L * cap, -1), w, sw, counts, [e * cap for e in range(L)],
+                  out.view(L * cap, 24), canary)
 
 
 def test_grouped_same_result_for_every_form_and_call():
@@ -400,6 +452,8 @@ def test_grouped_offsets_past_32_bits():
 LAYERS = [  # T, H, I, E, L, k, begin
     (1, 64, 32, 4, 4, 1, 0), (1, 7168, 96, 32, 32, 8, 0), (3, 96, 64, 8, 8, 2, 0), (5, 2592, 1056, 12, 6, 4, 3),
     (16, 256, 128, 8, 8, 2, 0), (17, 512, 160, 4, 2, 2, 1), (64, 256, 128, 8, 8, 2, 0), (128, 416, 224, 64, 8, 8, 8),
+    (2, 160, 96, 32, 32, 32, 0), (13, 64, 64, 128, 128, 5, 0), (13, 64, 64, 128, 100, 4, 20), (3, 16416, 32, 4, 4, 2, 0),
+    (9, 64, 8224, 3, 3, 1, 0), (40, 4128, 64, 16, 16, 3, 0), (128, 32, 32, 2048, 2048, 32, 0),
     (128, 64, 32, 1, 1, 1, 0), (128, 128, 64, 40, 40, 32, 0), (37, 2080, 544, 40, 40, 6, 0), (8, 64, 2080, 64, 4, 3, 60),
 ]
 
