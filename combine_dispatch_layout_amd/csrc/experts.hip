@@ -1066,8 +1066,15 @@ struct FewArgs {
     const uint8_t *w2, *w2_s;    // [L, H, I]
     uint16_t *out;               // [T, H]
     int32_t *lists;              // see FewLists
-    uint16_t *h;                 // [T k, I]
+    uint16_t *h;                 // [T k, I], twice for up to kSplitTokens tokens
 };
+
+// The activations between the products are rounded to bf16, the second
+// product's operand type.  Up to two tokens use 2 of its 16 columns: there the
+// rounding's remainder takes two more, at the price of a row load a turn
+// (one token, H = 7168, I = 2048, top-8: 44 us with either in MXFP4).
+constexpr int kSplitTokens = 2;
+constexpr int kSplitXt = 1;                     // the first kernel's column loads for them
 
 // Up to 64 slots, the routing lists hold the experts with slots in the order
 // of their first slot; above, all L experts.
@@ -1440,8 +1447,20 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(FewArgs a)
                 float h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i];
-                *reinterpret_cast<u32x2 *>(a.h + (int64_t)slot * a.I + i0 + 4 * g) =
-                    u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+                const u32x2 hi = {pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+                uint16_t *to = a.h + (int64_t)slot * a.I + i0 + 4 * g;
+                *reinterpret_cast<u32x2 *>(to) = hi;
+                if constexpr (kSplitXt == XT) {
+                    // what the rounding left (a non-finite value leaves nothing)
+                    float lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = i < 2 ? hi.x : hi.y;
+                        const float r = i & 1 ? bf16_hi(w) : bf16_lo(w);
+                        lo[i] = __builtin_isfinite(r) ? h[i] - r : 0.0f;
+                    }
+                    *reinterpret_cast<u32x2 *>(to + (int64_t)n * a.I) = u32x2{pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3])};
+                }
             }
         }
     }
@@ -1467,9 +1486,10 @@ struct FewDownLds {
     }
 };
 
-template <bool FP4, int WAVES>
+template <bool FP4, int WAVES, bool SPLIT>
 __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
 {
+    constexpr int kSlots = SPLIT ? kSplitTokens : kItemSlots;      // slots at a time
     constexpr int G = FP4 ? 2 : 8;             // a turn
     extern __shared__ u32x4 lds4[];
     uint8_t *lds = reinterpret_cast<uint8_t *>(lds4);
@@ -1510,7 +1530,7 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
     parts = parts < turns ? parts : turns;
     const int items = active * parts;
     const int c = lane & 15, g = lane >> 4;
-    const rsrc_t hr = make_rsrc(a.h, (uint32_t)n * I * 2);
+    const rsrc_t hr = make_rsrc(a.h, (uint32_t)n * I * (SPLIT ? 4 : 2));
 
     auto run = [&](auto rows2) {
         constexpr int XT = decltype(rows2)::value;
@@ -1527,11 +1547,13 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
         FewRows<FP4> rows[1] = {FewRows<FP4>(a.w2, a.w2_s, 0, 0, a.I)};
         uint32_t x_off[XT];
         auto set_slots = [&] {
-            const int live = count - c0 < kItemSlots ? count - c0 : kItemSlots;
+            const int live = count - c0 < kSlots ? count - c0 : kSlots;
 #pragma unroll
             for (int j = 0; j < XT; ++j) {
-                const int i = 2 * j + (lane >> 5);
-                x_off[j] = live > 0 ? (uint32_t)slots[first + c0 + (i < live ? i : 0)] * I * 2 : 0u;
+                // SPLIT: row i < 2 is slot i's activations, row 2 + i their remainder
+                const int i = SPLIT ? lane >> 5 : 2 * j + (lane >> 5);
+                const uint32_t part = SPLIT && j == 1 ? (uint32_t)n * I * 2 : 0u;
+                x_off[j] = live > 0 ? (uint32_t)slots[first + c0 + (i < live ? i : 0)] * I * 2 + part : 0u;
             }
             turn = turn0;
         };
@@ -1553,14 +1575,14 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
         // the next turn's operands; past the last item no memory is read and there are no slots
         auto load = [&](Turn &q) {
             q.begin = first + c0;
-            q.live = count - c0 < kItemSlots ? count - c0 : kItemSlots;
+            q.live = count - c0 < kSlots ? count - c0 : kSlots;
             q.d = count ? (uint32_t)turn * kTurn : I;
             q.last = turn + 1 == turn1;
             q.x.lds = lds + at.columns + (size_t)wave * kItemSlots * 512;
             q.x.load(hr, I, q.d, [&](int i) { return x_off[i / 2]; });
             q.w.template load<true>(rows, I, q.d, 0);
             if (++turn == turn1) {
-                c0 += kItemSlots;
+                c0 += kSlots;
                 if (c0 < count)
                     set_slots();
                 else
@@ -1572,6 +1594,13 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             q.x.store();
             q.w.multiply(acc, I, q.d, 0, [&](uint32_t i) { return q.x.chunk(i); }, [&](int i) { return q.w.scales(i); });
             if (!q.last) return;
+            if constexpr (SPLIT) {
+                // columns c and c + 2 of a quad
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[0][i] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(acc[0][i]), 0x4E,
+                                                                                      0xF, 0xF, false));
+            }
             const bool real = c < q.live;
             const int slot = slots[q.begin + (real ? c : 0)];
             const float wt = wts[slot];
@@ -1581,7 +1610,7 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             const int prev = __builtin_amdgcn_update_dpp(-1, t, 0x111, 0xF, 0xF, false);       // row_shr:1
             int rank = 0;
             if (__ballot(real && prev == t) != 0) {
-                for (int j = 1; j < kItemSlots; ++j) {
+                for (int j = 1; j < kSlots; ++j) {
                     const int pt = __shfl(t, (lane & ~15) + (c >= j ? c - j : 0), kWave);
                     if (c >= j && pt == t) ++rank;
                 }
@@ -1616,7 +1645,9 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             }
         }
     };
-    if (many)
+    if constexpr (SPLIT)
+        run(std::integral_constant<int, kSplitTokens>{});
+    else if (many)
         run(std::integral_constant<int, kItemSlots / 2>{});
     else
         run(std::integral_constant<int, 1>{});
@@ -1758,7 +1789,7 @@ inline int check_few(int64_t T, int32_t k, int64_t H, int64_t I, int32_t L)
     if (H < 1 || I < 1 || L < 1 || L > CDL_MAX_LOCAL_EXPERTS) return CDL_ERR_BAD_SIZE;
     if (H > CDL_MAX_HIDDEN || I > CDL_MAX_HIDDEN) return CDL_ERR_TOO_LARGE;
     // the token rows and the activations are addressed with 32-bit byte offsets
-    if (T * H > INT32_MAX - 8 || T * k * I > INT32_MAX - 8) return CDL_ERR_TOO_LARGE;
+    if (T * H > INT32_MAX - 8 || T * k * I * (T <= kSplitTokens ? 2 : 1) > INT32_MAX - 8) return CDL_ERR_TOO_LARGE;
     if (T > CDL_MOE_LAYER_MAX_TOKENS || T * k > kFewMaxSlots) return CDL_ERR_UNSUPPORTED;
     return CDL_OK;
 }
@@ -1771,7 +1802,8 @@ inline size_t few_list_bytes(int64_t T, int32_t k, int32_t L)
 
 inline size_t few_ws_bytes(int64_t T, int32_t k, int64_t I, int32_t L)
 {
-    return few_list_bytes(T, k, L) + (((size_t)(T * k) * (size_t)I * 2 + 255) & ~(size_t)255);
+    return few_list_bytes(T, k, L) +
+           (((size_t)(T * k) * (size_t)I * (T <= kSplitTokens ? 4 : 2) + 255) & ~(size_t)255);
 }
 
 template <bool FP4>
@@ -1791,8 +1823,8 @@ int run_few(FewArgs a, void *ws, hipStream_t stream)
         few_gate_up_kernel<FP4, decltype(xt)::value, decltype(sc)::value><<<grid1, dim3(kFewThreads), lds1, stream>>>(a);
     };
     auto launch_xt = [&](auto sc) {
-        if (a.T <= 2)
-            launch(std::integral_constant<int, 1>{}, sc);
+        if (a.T <= kSplitTokens)
+            launch(std::integral_constant<int, kSplitXt>{}, sc);
         else
             launch(std::integral_constant<int, 4>{}, sc);
     };
@@ -1812,13 +1844,26 @@ int run_few(FewArgs a, void *ws, hipStream_t stream)
     static_assert(8 * CDL_MOE_LAYER_MAX_TOKENS * 64 + 8 * kItemSlots * 512 + kFewMaxSlots * 10 + 16 <= 160 * 1024 &&
                       16 * 64 * 64 + 16 * kItemSlots * 512 + 2048 * 10 + 16 <= 160 * 1024,
                   "the second kernel's LDS");
-    const bool many = grid.x >= 256;
-    if (!many && a.T <= 64 && n <= 2048)
-        few_down_kernel<FP4, 16><<<grid, dim3(16 * kWave), FewDownLds(16, a.T, n, A).bytes, stream>>>(a);
-    else if (!many || a.T <= 64)
-        few_down_kernel<FP4, 8><<<grid, dim3(8 * kWave), FewDownLds(8, a.T, n, A).bytes, stream>>>(a);
-    else
-        few_down_kernel<FP4, 4><<<grid, dim3(4 * kWave), FewDownLds(4, a.T, n, A).bytes, stream>>>(a);
+    const bool fill = grid.x < 256;
+    auto down = [&](auto waves, auto split) {
+        constexpr int W = decltype(waves)::value;
+        few_down_kernel<FP4, W, decltype(split)::value><<<grid, dim3(W * kWave), FewDownLds(W, a.T, n, A).bytes, stream>>>(a);
+    };
+    const std::integral_constant<int, 16> w16;
+    const std::integral_constant<int, 8> w8;
+    const std::integral_constant<int, 4> w4;
+    if (a.T <= kSplitTokens) {
+        if (fill)
+            down(w16, std::true_type{});
+        else
+            down(w8, std::true_type{});
+    } else if (fill && a.T <= 64 && n <= 2048) {
+        down(w16, std::false_type{});
+    } else if (fill || a.T <= 64) {
+        down(w8, std::false_type{});
+    } else {
+        down(w4, std::false_type{});
+    }
     return launch_status();
 }
 

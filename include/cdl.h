@@ -599,7 +599,8 @@ size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
  *   h = g / (1 + exp(-g)) * u,  (g, u) = W13[e] x[t],  e = e_{t, j}
  *
  * with fp32 accumulation; h is rounded to bf16, the operand type of the
- * second product.  A token with no valid slot gets +0.
+ * second product (up to 2 tokens keep the remainder of that rounding, as a
+ * second bf16 value).  A token with no valid slot gets +0.
  *
  *   x             in  [T, H] bf16
  *   topk_ids, topk_weights, expert_begin, L   as for the layout and cdl_combine
@@ -610,7 +611,7 @@ size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
  *                     initialisation needed; calls that overlap need their own
  * T <= CDL_MOE_LAYER_MAX_TOKENS and T * k <= 4096 (CDL_ERR_UNSUPPORTED
  * otherwise: larger batches take the permute, the grouped products and the
- * combine); T * H and T * k * I below 2^31; H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte aligned.  The
+ * combine); T * H and T * k * I below 2^30; H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte aligned.  The
  * sums are taken in a fixed order: the result is deterministic.
  */
 int cdl_moe_layer(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,

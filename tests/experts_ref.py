@@ -72,8 +72,8 @@ def bf16_step(v):
 
 def layer(x, ids, wts, w13, w2, expert_begin):
     """(out [T, H], bound) of the MoE layer in 64 bits; x, w13 [L, 2 I, H], w2
-    [L, H, I] float64 values.  h is rounded to bf16 as the operator defines;
-    where the fp32 error could carry h over a rounding border the bound grows
+    [L, H, I] float64 values.  h is rounded to bf16 as the operator defines
+    (up to two tokens keep the remainder); where the fp32 error could carry h over a rounding border the bound grows
     by that step."""
     T, k = ids.shape
     L, I = w13.shape[0], w13.shape[1] // 2
@@ -87,9 +87,14 @@ def layer(x, ids, wts, w13, w2, expert_begin):
             continue
         gu, d = product(x[t], w13[e])
         h, dh = swiglu(gu[:, :I], d[:, :I], gu[:, I:], d[:, I:])
-        hr = h.to(torch.bfloat16).double()
-        step = bf16_step(hr)
-        flip = torch.where((h - hr).abs() + dh > step / 2 * (1 - 2.0 ** -10), step + dh, 0.0)
+        if T <= 2:
+            # h = hi + lo: the remainder is at most BF16 |h|, its rounding
+            # loses at most BF16 of it (lo is exact in fp32: hi is h's nearest)
+            hr, flip = h, dh + BF16 * BF16 * h.abs()
+        else:
+            hr = h.to(torch.bfloat16).double()
+            step = bf16_step(hr)
+            flip = torch.where((h - hr).abs() + dh > step / 2 * (1 - 2.0 ** -10), step + dh, 0.0)
         y, dy = product(hr, w2[e])
         dy = dy + flip @ w2[e].abs().t()
         w = wts[t, j].double().unsqueeze(1)

@@ -509,6 +509,8 @@ def test_layer_routing_edges(kind):
     mixed[1, :] = 2 ** 31 - 1
     mixed[2, 0] = -2 ** 31
     check_layer(kind, x, mixed, wts, w13, w2, 2)
+    one = torch.full((1, 4), 1, dtype=torch.int32, device=DEV)      # one token, four slots of one expert
+    check_layer(kind, x[:1].contiguous(), one, wts[:1].contiguous(), w13, w2, 0)
     twice = ids.clone()
     twice[:, 1] = twice[:, 0]
     twice[5, :] = 3
