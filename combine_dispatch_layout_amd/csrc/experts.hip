@@ -49,8 +49,9 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax16)
 // (255) and zero codes, so that the whole group reads back as NaN.
 // v_cvt_scalef32_pk_fp4_bf16 rounds x / 2^E to the nearest code, ties to the
 // even one, with E the exponent field of its scale operand read as an E8M0
-// code (field 0: 2^-127), and saturates at 6; checked on gfx950 over every
-// bf16 for fields 0 to 254.
+// code (field 0: 2^-127), and saturates at 6; checked on gfx950 for eleven
+// fields from 0 to 254 over every bf16 of up to 2^56 times the scale.  The
+// byte chosen here leaves no finite magnitude above 6 times the scale.
 __device__ __forceinline__ u32x2 mx_quant16(u32x4 a, u32x4 b, uint32_t *scale)
 {
     using u16x2 = unsigned short __attribute__((ext_vector_type(2)));
@@ -1771,9 +1772,10 @@ int launch_grouped_tiles(const GroupedArgs &a, hipStream_t stream)
 // Tiles of 256 token rows where the buffer has 64 rows or more an expert,
 // tiles of 64 below and for padded buffers of up to 256 rows an expert, which
 // are mostly empty in decode.  Measured, us for tiles of 64 and 256: 4096 rows
-// of 32 experts, K = 7168, N = 4096: 202 and 136; 131072 rows of 128 experts,
-// K = N = 4096: 2304 and 1355; padded, 128 tokens of top-8 over 32 of 256
-// experts, K = 7168, N = 4096: 95 and 104.
+// of 32 experts, K = 7168, N = 4096: 165 and 127-133; 9000 rows of 64 uneven
+// experts, K = 1440, N = 5000: 137 and 109; 131072 rows of 128 experts,
+// K = N = 4096: 2015 and 1269; padded, 128 tokens of top-8 over 32 of 256
+// experts, K = 7168, N = 4096: 88 and 93.
 template <bool SWIGLU>
 int launch_grouped(const GroupedArgs &a, hipStream_t stream)
 {
