@@ -533,6 +533,28 @@ def test_layer_nonfinite_rows_stay_apart(kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_layer_infinite_activations_stay_infinite(kind, T):
+    """g = u = 2^66 overflows h in fp32: its remainder is none, not inf - inf.
+    Sums of +inf times positive weights are +inf; other tokens are exact."""
+    announce("layer %s infinite h T=%d" % (kind, T))
+    H, I = 64, 32
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    x[0, 0] = 1.0
+    ids = torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+    wts = torch.full((T, 1), 0.5, device=DEV)
+    w13 = torch.zeros(1, 2 * I, H, dtype=torch.bfloat16, device=DEV)
+    w13[:, :, 0] = 2.0 ** 66
+    w2 = torch.ones(1, H, I, dtype=torch.bfloat16, device=DEV)
+    if kind == "bf16":
+        out = cdl.moe_layer(x, ids, wts, w13, w2)
+    else:
+        out = cdl.moe_layer_mxfp4(x, ids, wts, *cdl.quant_mxfp4(w13), *cdl.quant_mxfp4(w2))
+    assert bool((out[0] == float("inf")).all())
+    assert bool((out[1:] == 0).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
 def test_layer_is_deterministic_on_a_side_stream(kind):
     a = layer_inputs(50, 512, 256, 16, 16, 4)
     ref, _, _ = run_layer(kind, *a, 0)
