@@ -1716,7 +1716,21 @@ int launch_mx_permute_self(const PermuteArgs &a, const uint16_t *x, int64_t H, u
     return launch_status();
 }
 
-// Larger ones count their superblocks first.
+// Longer batches take the layout's own kernels, then the scatter: the layout
+// wave of every workgroup adds up the counts of all superblocks, work that
+// grows with T and L in each of T / 4 workgroups, and its rows wait for it.
+// Wide rows hide more of it.  Measured, us for one launch after the count and
+// for the separate layout, top-8, all experts local, T = 2560 / 4096 / 8192:
+// H = 2048, L = 128: 19.9 and 24.7 / 30.8 and 27.0 / 62.5 and 39.4;
+// H = 7168, L = 128: 27.6 and 34.1 / 46.3 and 47.9 / 108.8 and 101.6;
+// H = 16384, 32 of 256 experts: 22.3 and 28.0 / 33.6 and 37.0 / 57.4 and 62.1
+// (16384 tokens: top-8 109 and 121, top-2 52 and 47; 32768, top-2: 114 and 83).
+inline bool mx_layout_apart(int64_t T, int64_t H)
+{
+    return T >= (H <= 4096 ? 4096 : H <= kMxPairs * 1024 ? 5121 : 16385);
+}
+
+// Batches in between count their superblocks first.
 int launch_mx_permute(PermuteArgs a, const uint16_t *x, int64_t H, uint8_t *q, uint8_t *s, void *ws,
                       hipStream_t stream)
 {
@@ -1972,6 +1986,12 @@ int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
     a.cap_rows = cap_rows;
     if (T == 0) return run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
     if (T * k <= kMxSelfSlots) return launch_mx_permute_self<false>(a, x, H, out_q, out_scales, (hipStream_t)stream);
+    if (mx_layout_apart(T, H)) {
+        rc = run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
+        if (rc != CDL_OK) return rc;
+        return launch_mx_scatter<false>(x, T, H, k, src2dst, out_q, out_scales, cap_rows, status, MxLL{},
+                                        (hipStream_t)stream);
+    }
     return launch_mx_permute(a, x, H, out_q, out_scales, ws, (hipStream_t)stream);
 }
 

@@ -102,6 +102,10 @@ SCATTER = [  # T, H, E, L, k, begin, alignment, dist
     (5000, 64, 128, 128, 8, 0, 1, "zipf"), (40, 128, 64, 2, 64, 3, 1, "uniform"),
     (512, 64, 16, 16, 8, 0, 1, "uniform"), (513, 96, 16, 5, 7, 2, 32, "uniform"), (2048, 64, 4, 4, 2, 0, 1, "uniform"),
     (4097, 32, 4, 3, 1, 0, 1, "zipf"), (64, 64, 2048, 2048, 64, 0, 1, "uniform"), (65, 64, 2048, 2048, 64, 0, 4, "uniform"),
+    # both sides of the borders where the layout leaves the rows' launch
+    (4095, 64, 32, 8, 2, 1, 16, "zipf"), (4096, 64, 32, 8, 2, 1, 16, "zipf"), (4096, 4096, 16, 4, 2, 3, 1, "uniform"),
+    (4096, 4128, 16, 4, 2, 3, 1, "uniform"), (5120, 4128, 16, 4, 2, 0, 8, "zipf"), (5121, 4128, 16, 4, 2, 0, 8, "zipf"),
+    (16385, 32, 256, 256, 8, 0, 128, "zipf"),
 ]
 
 
@@ -149,6 +153,20 @@ def test_scatter_into_too_few_rows():
     assert int(st.item()) == cdl.CDL_STATUS_ROWS_OVERFLOW
     assert torch.equal(q[:90], full[:90]) and torch.equal(s[:90], fs[:90])
     assert bool((q[90:] == CANARY).all()) and bool((s[90:] == CANARY).all())
+
+
+def test_long_permute_into_too_few_rows():
+    x, ids, _ = scatter_inputs(4500, 64, 16, 4, 4, 2, "uniform")
+    lay = cdl.dispatch_layout(ids.to(DEV), 2, 4)
+    full, fs = cdl.dispatch_mxfp4(x.to(DEV), lay)
+    n = full.shape[0] - 37
+    st = status_word()
+    q = torch.full((n + 5, 32), CANARY, dtype=torch.uint8, device=DEV)
+    s = torch.full((n + 5, 2), CANARY, dtype=torch.uint8, device=DEV)
+    cdl.permute_mxfp4(x.to(DEV), ids.to(DEV), 2, 4, out_q=q[:n], out_scales=s[:n], status=st)
+    assert int(st.item()) == cdl.CDL_STATUS_ROWS_OVERFLOW
+    assert torch.equal(q[:n], full[:n]) and torch.equal(s[:n], fs[:n])
+    assert bool((q[n:] == CANARY).all()) and bool((s[n:] == CANARY).all())
 
 
 @pytest.mark.parametrize("T,H,E,L,k,b,cap", [(128, 7168, 256, 32, 8, 0, 128), (64, 256, 8, 8, 2, 0, 9),
