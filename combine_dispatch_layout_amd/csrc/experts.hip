@@ -1789,12 +1789,17 @@ int launch_grouped_tiles(const GroupedArgs &a, hipStream_t stream)
 // of 32 experts, K = 7168, N = 4096: 165 and 127-133; 9000 rows of 64 uneven
 // experts, K = 1440, N = 5000: 137 and 109; 131072 rows of 128 experts,
 // K = N = 4096: 2015 and 1269; padded, 128 tokens of top-8 over 32 of 256
-// experts, K = 7168, N = 4096: 88 and 93.
+// experts, K = 7168, N = 4096: 88 and 93.  At 64 rows an expert drawn at
+// random (32 experts, K = 7168, N = 4096) 120 and 108, at 32 rows 93 and 100.
+// Tiles of 64 also where they are expected to give every workgroup one at most
+// (segments of random length take half a tile more each): 8 experts of 96 rows,
+// K = 7168, N = 4096: 38 and 46; of 128 rows, 320 tiles, 65 and 54.
 template <bool SWIGLU>
 int launch_grouped(const GroupedArgs &a, hipStream_t stream)
 {
     if (a.rows == 0) return CDL_OK;
-    const bool large = a.seg ? a.rows / a.L >= 64 : a.cap > 256;
+    const int64_t small_tiles = (a.rows / 64 + a.L / 2) * ((a.N + kGroupedNT - 1) / kGroupedNT);
+    const bool large = a.seg ? a.rows / a.L >= 64 && small_tiles > kGroupedWgs : a.cap > 256;
     return large ? launch_grouped_tiles<256, SWIGLU>(a, stream) : launch_grouped_tiles<64, SWIGLU>(a, stream);
 }
 

@@ -231,6 +231,9 @@ COUNTS = [
     ([128] * 4, 512, 512), ([7, 200, 65, 0, 1, 300], 1440, 500), ([100, 28], 7168, 136), ([1] * 70, 160, 33),
     ([257, 255, 256], 2048, 264), ([3, 0, 9, 16, 2], 7168, 1032), ([600], 288, 1000), ([17] * 33, 544, 72),
     ([48, 96], 15 * 32, 2000),
+    # more than 256 tiles of 64 rows, 64 rows an expert or more: the large tile
+    ([64, 1, 0, 330], 96, 8200), ([257, 255, 256], 2048, 5000), ([7, 200, 65, 0, 1, 300], 1440, 7000),
+    ([600], 288, 7400), ([100, 428], 7168, 8000), ([4136, 17], 64, 1000),
 ]
 
 
@@ -262,7 +265,8 @@ def test_grouped(counts, K, N, form):
 
 
 @pytest.mark.parametrize("shift", [1, 2, 3])
-@pytest.mark.parametrize("counts,K,N", [([70, 3], 1056, 260), ([300, 212], 736, 40), ([20, 90, 1], 2048, 513)])
+@pytest.mark.parametrize("counts,K,N", [([70, 3], 1056, 260), ([300, 212], 736, 40), ([20, 90, 1], 2048, 513),
+                                        ([300, 212], 736, 8256), ([300, 213], 1056, 8191)])
 def test_grouped_scales_at_any_byte(counts, K, N, shift):
     """Scale tensors that start at any byte, rows of an odd number of scales,
     output rows at 2-byte alignment; the scales' neighbours are NaN codes."""
@@ -397,7 +401,9 @@ def check_swiglu(a, sa, w, sw, q, s, I):
 
 @pytest.mark.parametrize("counts,K,I", [([1], 32, 32), ([5, 0, 70], 96, 64), ([64, 130], 256, 256),
                                         ([7, 200, 65, 0, 1], 1440, 544), ([100, 28], 7168, 160),
-                                        ([257, 255], 2048, 288), ([3, 9, 16], 7168, 1056)])
+                                        ([257, 255], 2048, 288), ([3, 9, 16], 7168, 1056),
+                                        ([257, 255], 2048, 4128), ([70, 200, 65, 0, 61], 1440, 4160),
+                                        ([300, 212], 96, 4128)])
 @pytest.mark.parametrize("form", ["segments", "masked"])
 def test_grouped_swiglu(counts, K, I, form):
     announce("grouped swiglu %s counts=%s K=%d I=%d" % (form, counts, K, I))
