@@ -1596,11 +1596,15 @@ __global__ __launch_bounds__(WAVES *kWave) void few_down_kernel(FewArgs a)
             q.w.multiply(acc, I, q.d, 0, [&](uint32_t i) { return q.x.chunk(i); }, [&](int i) { return q.w.scales(i); });
             if (!q.last) return;
             if constexpr (SPLIT) {
-                // columns c and c + 2 of a quad
+                // columns c and c + 2 of a quad; an infinite or NaN weight makes
+                // the value's sum what it has to be and the remainder's anything
+                // (infinity times 0 or the other sign), so that one is left out
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[0][i] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(acc[0][i]), 0x4E,
-                                                                                      0xF, 0xF, false));
+                for (int i = 0; i < 4; ++i) {
+                    const float rest = __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                        0, (int)__float_as_uint(acc[0][i]), 0x4E, 0xF, 0xF, false));
+                    acc[0][i] += __builtin_isfinite(rest) ? rest : 0.0f;
+                }
             }
             const bool real = c < q.live;
             const int slot = slots[q.begin + (real ? c : 0)];
