@@ -1776,10 +1776,10 @@ int launch_grouped_tiles(const GroupedArgs &a, hipStream_t stream)
     constexpr int kCols = SWIGLU ? kGroupedNT / 2 : kGroupedNT;
     const int64_t tiles_n = ((SWIGLU ? a.N / 2 : a.N) + kCols - 1) / kCols;
     // Tiles are numbered in 32 bits, whatever counts the device arrays hold
-    // (each is cut to the buffer); every expert adds at most one partly filled
-    // row tile.
+    // (each is cut to the buffer), with room for a workgroup's step past the
+    // last one; every expert adds at most one partly filled row tile.
     const int64_t most = a.seg ? a.rows : a.cap;
-    if ((most + MT - 1) / MT * tiles_n > INT32_MAX / a.L) return CDL_ERR_TOO_LARGE;
+    if ((most + MT - 1) / MT * tiles_n > (INT32_MAX - kGroupedWgs) / a.L) return CDL_ERR_TOO_LARGE;
     const int64_t tiles_m = a.seg ? a.rows / MT + a.L : (int64_t)a.L * ((a.cap + MT - 1) / MT);
     const int64_t tiles = (tiles_m * tiles_n + 7) / 8 * 8;
     grouped_kernel<MT, SWIGLU><<<dim3((unsigned)(tiles < kGroupedWgs ? tiles : kGroupedWgs)), dim3(kGroupedThreads),

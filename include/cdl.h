@@ -564,7 +564,7 @@ int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
  *                      CDL_STATUS_LL_OVERFLOW (padded)
  * K % 32 == 0, q and w_q 16-byte aligned; any N >= 1.  CDL_ERR_TOO_LARGE
  * where L times the output tiles of one expert that owns the whole buffer (64
- * rows, 256 columns) reaches 2^31.
+ * rows, 256 columns) exceeds 2^31 - 257.
  */
 int cdl_grouped_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t K,
                       const uint8_t *w_q, const uint8_t *w_scales, int32_t L, int64_t N,

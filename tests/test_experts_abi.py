@@ -109,3 +109,13 @@ def test_binding_refuses_cpu_tensors():
                   lambda: cdl.moe_layer_mxfp4(bf, ids, wts, u8[None], s[None], u8[None], s[None])):
         with pytest.raises(ValueError, match="GPU"):
             call_()
+
+
+def test_grouped_tile_numbers_leave_room_for_a_step():
+    """Device counts may claim the whole buffer for every expert.  1302 experts
+    of 49981 x 33 tiles are 2^31 - 2 tiles: a workgroup's step past the last
+    tile would not fit 32 bits."""
+    over = dict(rows=49981 * 256, N=33 * 256, L=1302)
+    assert 1302 * 49981 * 33 == 2 ** 31 - 2
+    assert call("cdl_grouped_mxfp4", GROUPED, **over) == EBIG
+    assert call("cdl_grouped_swiglu_mxfp4", SWIGLU, rows=49981 * 256, I=33 * 128, L=1302) == EBIG
