@@ -1781,7 +1781,7 @@ int launch_grouped_tiles(const GroupedArgs &a, hipStream_t stream)
     const int64_t most = a.seg ? a.rows : a.cap;
     if ((most + MT - 1) / MT * tiles_n > (INT32_MAX - kGroupedWgs) / a.L) return CDL_ERR_TOO_LARGE;
     const int64_t tiles_m = a.seg ? a.rows / MT + a.L : (int64_t)a.L * ((a.cap + MT - 1) / MT);
-    const int64_t tiles = (tiles_m * tiles_n + 7) / 8 * 8;
+    const int64_t filled = (tiles_m * tiles_n + 7) / 8 * 8, tiles = filled ? filled : 8;     // (none: the counts' check)
     grouped_kernel<MT, SWIGLU><<<dim3((unsigned)(tiles < kGroupedWgs ? tiles : kGroupedWgs)), dim3(kGroupedThreads),
                                  GroupedShape<MT>::kLds + (size_t)a.L * sizeof(int32_t), stream>>>(a, (int)tiles_n);
     return launch_status();
@@ -1801,7 +1801,8 @@ int launch_grouped_tiles(const GroupedArgs &a, hipStream_t stream)
 template <bool SWIGLU>
 int launch_grouped(const GroupedArgs &a, hipStream_t stream)
 {
-    if (a.rows == 0) return CDL_OK;
+    // (an empty buffer: only the check of the counts is left)
+    if (a.rows == 0 && !a.status) return CDL_OK;
     const int64_t small_tiles = (a.rows / 64 + a.L / 2) * ((a.N + kGroupedNT - 1) / kGroupedNT);
     const bool large = a.seg ? a.rows / a.L >= 64 && small_tiles > kGroupedWgs : a.cap > 256;
     return large ? launch_grouped_tiles<256, SWIGLU>(a, stream) : launch_grouped_tiles<64, SWIGLU>(a, stream);

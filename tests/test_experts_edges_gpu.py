@@ -4,10 +4,36 @@ import pytest
 import torch
 
 import combine_dispatch_layout_amd as cdl
-from gpu_util import DEV, announce
-from test_experts_gpu import layer_inputs
+from gpu_util import DEV, announce, status_word
+from test_experts_gpu import gen, layer_inputs, mx_random
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# grouped product
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("L", [2, 70])
+@pytest.mark.parametrize("counts,flag", [(0, 0), (3, 1), (-1, 1)])
+def test_grouped_counts_of_an_empty_buffer(L, counts, flag):
+    """A buffer of no rows: counts that are not zero do not fit it and are
+    flagged, as in any other buffer."""
+    announce("grouped, no rows, L=%d counts=%d" % (L, counts))
+    g = gen(L)
+    w, sw = mx_random(g, L, 64, 64)
+    c = torch.zeros(L, dtype=torch.int32, device=DEV)
+    c[L - 1] = counts
+    none = torch.empty(0, 32, dtype=torch.uint8, device=DEV), torch.empty(0, 2, dtype=torch.uint8, device=DEV)
+    padded = [t.new_empty(L, 0, t.shape[1]) for t in none]
+    seg = torch.zeros(L + 1, dtype=torch.int64, device=DEV)
+    for call in (cdl.grouped_mxfp4, cdl.grouped_swiglu_mxfp4):
+        st = status_word()
+        call(*none, w, sw, c, seg, status=st)
+        assert int(st.item()) == flag * cdl.CDL_STATUS_ROWS_OVERFLOW
+        st = status_word()
+        call(*padded, w, sw, c, status=st)
+        assert int(st.item()) == flag * cdl.CDL_STATUS_LL_OVERFLOW
 
 
 # ---------------------------------------------------------------------------
