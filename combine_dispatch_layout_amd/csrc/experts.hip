@@ -1808,6 +1808,14 @@ int launch_grouped(const GroupedArgs &a, hipStream_t stream)
     return large ? launch_grouped_tiles<256, SWIGLU>(a, stream) : launch_grouped_tiles<64, SWIGLU>(a, stream);
 }
 
+// Tokens whose activations the workspace holds: up to kSplitTokens have the
+// remainders as well, and a batch takes no less than a smaller one.
+inline int64_t few_act_tokens(int64_t T)
+{
+    const int64_t split = 2 * (T < kSplitTokens ? T : kSplitTokens);
+    return T > split ? T : split;
+}
+
 inline int check_few(int64_t T, int32_t k, int64_t H, int64_t I, int32_t L)
 {
     int rc = check_tk(T, k);
@@ -1815,7 +1823,7 @@ inline int check_few(int64_t T, int32_t k, int64_t H, int64_t I, int32_t L)
     if (H < 1 || I < 1 || L < 1 || L > CDL_MAX_LOCAL_EXPERTS) return CDL_ERR_BAD_SIZE;
     if (H > CDL_MAX_HIDDEN || I > CDL_MAX_HIDDEN) return CDL_ERR_TOO_LARGE;
     // the token rows and the activations are addressed with 32-bit byte offsets
-    if (T * H > INT32_MAX - 8 || T * k * I * (T <= kSplitTokens ? 2 : 1) > INT32_MAX - 8) return CDL_ERR_TOO_LARGE;
+    if (T * H > INT32_MAX - 8 || few_act_tokens(T) * k * I > INT32_MAX - 8) return CDL_ERR_TOO_LARGE;
     if (T > CDL_MOE_LAYER_MAX_TOKENS || T * k > kFewMaxSlots) return CDL_ERR_UNSUPPORTED;
     return CDL_OK;
 }
@@ -1828,8 +1836,7 @@ inline size_t few_list_bytes(int64_t T, int32_t k, int32_t L)
 
 inline size_t few_ws_bytes(int64_t T, int32_t k, int64_t I, int32_t L)
 {
-    return few_list_bytes(T, k, L) +
-           (((size_t)(T * k) * (size_t)I * (T <= kSplitTokens ? 4 : 2) + 255) & ~(size_t)255);
+    return few_list_bytes(T, k, L) + (((size_t)(few_act_tokens(T) * k) * (size_t)I * 2 + 255) & ~(size_t)255);
 }
 
 template <bool FP4>

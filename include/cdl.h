@@ -587,7 +587,8 @@ int cdl_grouped_swiglu_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t ro
 /*
  * cdl_moe_layer_workspace_size -- device workspace bytes of cdl_moe_layer and
  * cdl_moe_layer_mxfp4 (routing lists and the activations between the two
- * products); 0 for sizes they reject.
+ * products); 0 for sizes they reject.  It does not shrink as T grows: the
+ * workspace of the largest batch serves every smaller one.
  */
 size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
 
@@ -611,8 +612,10 @@ size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
  *                     initialisation needed; calls that overlap need their own
  * T <= CDL_MOE_LAYER_MAX_TOKENS and T * k <= 4096 (CDL_ERR_UNSUPPORTED
  * otherwise: larger batches take the permute, the grouped products and the
- * combine); T * H and T * k * I below 2^30; H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte aligned.  The
- * sums are taken in a fixed order: the result is deterministic.
+ * combine); T * H and T' * k * I at most 2^31 - 9, T' = max(T, 2 min(T, 2))
+ * (CDL_ERR_TOO_LARGE); H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte
+ * aligned, out 4-byte aligned.  The sums are taken in a fixed order: the
+ * result is deterministic.
  */
 int cdl_moe_layer(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,
                   const float *topk_weights, int32_t expert_begin, int32_t L, int64_t I,

@@ -119,3 +119,27 @@ def test_grouped_tile_numbers_leave_room_for_a_step():
     assert 1302 * 49981 * 33 == 2 ** 31 - 2
     assert call("cdl_grouped_mxfp4", GROUPED, **over) == EBIG
     assert call("cdl_grouped_swiglu_mxfp4", SWIGLU, rows=49981 * 256, I=33 * 128, L=1302) == EBIG
+
+
+@pytest.mark.parametrize("k,I,L", [(1, 32, 1), (8, 2048, 32), (6, 1056, 40), (32, 64, 2048), (64, 96, 300), (2, 1 << 22, 4)])
+def test_layer_workspace_grows_with_the_batch(k, I, L):
+    """A workspace of the largest batch serves every smaller one."""
+    f = cdl.library().cdl_moe_layer_workspace_size
+    most = min(128, 4096 // k)
+    sizes = [f(T, k, I, L) for T in range(most + 1)]
+    assert all(0 < a <= b for a, b in zip(sizes, sizes[1:])), sizes[:5]
+
+
+def test_layer_sizes_at_the_32_bit_limit():
+    """Byte offsets into the token rows and the activations stay below 2^32: T
+    * H, and the activations' elements of T tokens (4 tokens' from 2 to 4, 2
+    tokens' for one), reach 2^31 - 9 at most.  The workspace's size is asked for only
+    of sizes that are taken."""
+    H = 1 << 24
+    for name, base in (("cdl_moe_layer", LAYER), ("cdl_moe_layer_mxfp4", LAYER4)):
+        assert call(name, base, T=127, H=H, wsb=64) == EWS
+        assert call(name, base, T=128, H=H, wsb=64) == EBIG
+        for k, T, most in ((64, 2, 4), (64, 3, 4), (64, 4, 4), (64, 1, 2), (64, 5, 5)):
+            I = (2 ** 31 - 9) // (most * k) // 32 * 32
+            assert call(name, base, T=T, k=k, I=I, wsb=64) == EWS, (T, I)
+            assert call(name, base, T=T, k=k, I=I + 32, wsb=64) == EBIG, (T, I)

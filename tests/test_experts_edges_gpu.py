@@ -5,7 +5,7 @@ import torch
 
 import combine_dispatch_layout_amd as cdl
 from gpu_util import DEV, announce, status_word
-from test_experts_gpu import gen, layer_inputs, mx_random
+from test_experts_gpu import check_layer, gen, layer_inputs, mx_random
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,16 @@ def test_layer_infinite_and_nan_weights(kind, T):
     assert torch.equal(torch.isnan(out), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(out.double(), nan=0.0, posinf=1.0, neginf=-1.0),
                        torch.nan_to_num(want, nan=0.0, posinf=1.0, neginf=-1.0))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+def test_layer_smaller_batches_in_one_workspace(kind):
+    """The workspace of three tokens serves two and one; nothing behind its
+    size is written."""
+    H, I, L, k = 128, 96, 8, 4
+    size = cdl.moe_layer_workspace_size(3, k, I, L)
+    ws = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    for T in (3, 2, 1):
+        announce("layer %s T=%d in the workspace of 3" % (kind, T))
+        check_layer(kind, *layer_inputs(T, H, I, L, L, k), 0, workspace=ws[:size])
+        assert bool((ws[size:] == 0xA5).all())
