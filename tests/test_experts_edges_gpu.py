@@ -4,8 +4,9 @@ import pytest
 import torch
 
 import combine_dispatch_layout_amd as cdl
+import experts_check as C
 from gpu_util import DEV, announce, status_word
-from test_experts_gpu import check_layer, gen, layer_inputs, mx_random
+from test_experts_gpu import gen, layer_inputs, mx_random, run_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -79,5 +80,7 @@ def test_layer_smaller_batches_in_one_workspace(kind):
     ws = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device=DEV)
     for T in (3, 2, 1):
         announce("layer %s T=%d in the workspace of 3" % (kind, T))
-        check_layer(kind, *layer_inputs(T, H, I, L, L, k), 0, workspace=ws[:size])
+        a = layer_inputs(T, H, I, L, L, k)
+        out, v13, v2 = run_layer(kind, *a, 0, workspace=ws[:size])
+        C.check_layer_output(out, *a[:3], v13, v2, 0)
         assert bool((ws[size:] == 0xA5).all())
