@@ -5,6 +5,7 @@ import torch
 
 import combine_dispatch_layout_amd as cdl
 import experts_check as C
+import experts_ref as R
 from gpu_util import DEV, announce, status_word
 from test_experts_gpu import gen, layer_inputs, mx_random, run_layer
 
@@ -35,6 +36,91 @@ def test_grouped_counts_of_an_empty_buffer(L, counts, flag):
         st = status_word()
         call(*padded, w, sw, c, status=st)
         assert int(st.item()) == flag * cdl.CDL_STATUS_LL_OVERFLOW
+
+
+FAR = (0, 31, 127, 128, 255, 256, 511, 4096, 131071, 131072, 200000, 262143)      # bytes of a row of 2^19 elements
+
+
+def far_rows(g, q, s):
+    """Random codes at the FAR bytes of rows q (zero elsewhere), random scales
+    at their groups: dense rows of those elements alone, and their scales.
+    Products of two such rows are multiples of 2^-2 below 2^20, so their
+    fp32 sums are exact in any order."""
+    at = torch.tensor(FAR, device=DEV)
+    q[..., at] = torch.randint(0, 256, (*q.shape[:-1], len(FAR)), generator=g, device=DEV, dtype=torch.uint8)
+    s[..., at // 16] = torch.randint(127, 132, (*s.shape[:-1], len(FAR)), generator=g, device=DEV,
+                                     dtype=torch.int32).to(torch.uint8)
+    grid = torch.tensor(R.GRID + tuple(-v for v in R.GRID), dtype=torch.float64, device=DEV)
+    codes = q[..., at]
+    v = torch.stack((grid[(codes & 15).long()], grid[(codes >> 4).long()]), -1)
+    return (v * torch.exp2(s[..., at // 16].double() - 127).unsqueeze(-1)).flatten(-2)
+
+
+def test_grouped_far_weights_and_rows():
+    """Weights of an expert and rows of a segment more than 4 GiB from their
+    tensors' start, exact sums: another expert's or row's operands, or another
+    row's scales, give other numbers."""
+    announce("grouped, far weights and rows")
+    L, N, K = 5, 4096, 1 << 19                                        # 1 GiB of codes an expert
+    g = gen(2)
+    w = torch.zeros(L, N, K // 2, dtype=torch.uint8, device=DEV)
+    sw = torch.full((L, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    counts, seg = [3, 0, 2, 0, 5], [0, 3, 9000, 9002, 18000, 18005]   # row 18000 is 4.4 GiB in
+    a = torch.zeros(18005, K // 2, dtype=torch.uint8, device=DEV)
+    sa = torch.full((18005, K // 32), 127, dtype=torch.uint8, device=DEV)
+    vw, va = [far_rows(g, w[e], sw[e]) for e in range(L)], far_rows(g, a, sa)
+    out = torch.full((18005, N), -7.5, dtype=torch.bfloat16, device=DEV)
+    cdl.grouped_mxfp4(a, sa, w, sw, torch.tensor(counts, dtype=torch.int32, device=DEV),
+                      torch.tensor(seg, device=DEV), out=out)
+    want = torch.full_like(out, -7.5)
+    for e, c in enumerate(counts):
+        at = slice(seg[e], seg[e] + c)
+        want[at] = (va[at] @ vw[e].t()).to(torch.bfloat16)
+        assert c == 0 or not torch.equal(want[at], (va[at] @ vw[(e + 1) % L].t()).to(torch.bfloat16))
+    assert torch.equal(out, want)
+
+
+def test_grouped_far_outputs():
+    """Output rows (bf16, and MXFP4 behind SwiGLU) more than 4 GiB from the
+    tensors' start; products of 32 elements at equal scales are exact."""
+    announce("grouped, far outputs")
+    g = gen(3)
+    R1, L, N, K = 300001, 2, 8192, 32                                 # 4.6 GiB of output
+    a, sa = mx_random(g, R1, K, lo=127, hi=127)
+    w, sw = mx_random(g, L, N, K, lo=127, hi=127)
+    counts, seg = [149000, R1 - 149003], [0, 149003, R1]
+    dev = torch.tensor(counts, dtype=torch.int32, device=DEV), torch.tensor(seg, device=DEV)
+    out = torch.full((R1, N), -7.5, dtype=torch.bfloat16, device=DEV)
+    cdl.grouped_mxfp4(a, sa, w, sw, *dev, out=out)
+    for e in range(L):
+        v = R.values(w[e], sw[e])
+        for r in range(seg[e], seg[e] + counts[e], 20000):
+            at = slice(r, min(r + 20000, seg[e] + counts[e]))
+            assert torch.equal(out[at], (R.values(a[at], sa[at]) @ v.t()).to(torch.bfloat16)), (e, r)
+    assert bool((out[149000:149003] == -7.5).all())
+    del out
+    I = 32768                                                         # 4.6 GiB of codes
+    w, sw = mx_random(g, L, 2 * I, K, lo=124, hi=124)
+    q, s = cdl.grouped_swiglu_mxfp4(a, sa, w, sw, *dev)
+    for e, r in ((0, 0), (0, 148950), (1, 149003), (1, R1 - 50)):
+        at = slice(r, r + 50)
+        C.check_swiglu(a[at], sa[at], w[e], sw[e], q[at], s[at], I)
+
+
+def test_far_quantised_rows():
+    """Rows and read-back values more than 4 GiB from the tensors' start."""
+    announce("quantise, far rows")
+    rows, H = 20000, 131072                                           # 4.9 GiB of bf16
+    x = torch.zeros(rows, H, dtype=torch.bfloat16, device=DEV)
+    at = [0, 1, 16383, 16384, 16385, rows - 1]
+    x[at] = torch.randn(len(at), H, generator=gen(4), device=DEV).to(torch.bfloat16)
+    q, s = cdl.quant_mxfp4(x)
+    near = cdl.quant_mxfp4(x[at].contiguous())
+    assert torch.equal(q[at], near[0]) and torch.equal(s[at], near[1])
+    out = cdl.dequant_mxfp4(q, s)
+    assert torch.equal(out[at].double(), R.values(*near))
+    out[at] = 0
+    assert not bool(out.any())
 
 
 # ---------------------------------------------------------------------------
