@@ -38,6 +38,47 @@ def test_grouped_counts_of_an_empty_buffer(L, counts, flag):
         assert int(st.item()) == flag * cdl.CDL_STATUS_LL_OVERFLOW
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K,N", [(1056, 5056), (64, 6400), (7168, 4992)])
+def test_grouped_forms_give_the_same_bits(K, N, swiglu):
+    """A row's result is the same in plain and padded segments and in padded
+    buffers, with tiles of 64 rows (up to 256 rows an expert in a padded
+    buffer) and of 256."""
+    announce("grouped forms K=%d N=%d swiglu=%d" % (K, N, swiglu))
+    g = gen(K + N)
+    counts = [150, 40, 0, 256, 256, 8]                # segments: 280 tiles of 64 rows and more, so the large tile
+    L, rows = len(counts), sum(counts)
+    w, sw = mx_random(g, L, N, K, lo=118, hi=121)
+    a, sa = mx_random(g, rows, K, lo=122, hi=126)
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+
+    def run(begins, total, shape, seg):
+        """The live rows of a buffer of `total` rows, expert e's from begins[e] on."""
+        q = torch.zeros(total, K // 2, dtype=torch.uint8, device=DEV)
+        s = torch.zeros(total, K // 32, dtype=torch.uint8, device=DEV)
+        live, first = [], 0
+        for e, n in enumerate(counts):
+            q[begins[e]:begins[e] + n], s[begins[e]:begins[e] + n] = a[first:first + n], sa[first:first + n]
+            live += range(begins[e], begins[e] + n)
+            first += n
+        call = cdl.grouped_swiglu_mxfp4 if swiglu else cdl.grouped_mxfp4
+        out = call(q.view(*shape, -1), s.view(*shape, -1), w, sw, c, seg)
+        return [o.reshape(total, -1)[live] for o in (out if swiglu else (out,))]
+
+    def segments(align, gap):
+        seg = [0]
+        for n in counts:
+            seg.append(seg[-1] + (n + align - 1) // align * align + gap)
+        return run(seg[:-1], seg[-1], (seg[-1],), torch.tensor(seg, device=DEV))
+
+    def padded(cap):
+        return run([e * cap for e in range(L)], L * cap, (L, cap), None)
+
+    first = padded(256)
+    for other in (padded(257), padded(700), segments(1, 0), segments(16, 3), segments(128, 500)):
+        assert all(torch.equal(x, y) for x, y in zip(first, other))
+
+
 FAR = (0, 31, 127, 128, 255, 256, 511, 4096, 131071, 131072, 200000, 262143)      # bytes of a row of 2^19 elements
 
 
