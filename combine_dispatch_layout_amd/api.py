@@ -910,7 +910,9 @@ def grouped_mxfp4(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_sc
     accumulation.  w_q [L, N, K / 2].  With seg_indptr, q is [rows, K / 2] and
     expert e owns the counts[e] rows from seg_indptr[e]; without, q is the
     padded [L, cap, K / 2] buffer and counts its masked_m.  Rows of no expert
-    are left as they were.  Returns out [rows, N] or [L, cap, N]."""
+    are left as they were.  A quantised infinity is the number 6 * 2^127 here
+    (the format has none), so it need not make its results infinite; a NaN
+    does make them NaN.  Returns out [rows, N] or [L, cap, N]."""
     lead, K, L, N, cap = _grouped_args(q, scales, w_q, w_scales, counts, seg_indptr, status)
     if out is None:
         out = torch.empty(*lead, N, dtype=torch.bfloat16, device=q.device)

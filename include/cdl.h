@@ -487,10 +487,15 @@ int cdl_combine_timed(const uint16_t *y, int64_t y_rows, int64_t H, const int32_
  * Quantisation of a group: e is the smallest integer >= -127 with
  * 6 * 2^e >= amax (nothing saturates), each code the one nearest to x / 2^e,
  * ties to the even code, the sign kept (of zeros too); a zero group has e =
- * -127.  Non-finite values: a group with an infinity takes e = 127, so that
- * it reads back as infinity (its finite elements keep what 2^127 leaves of
- * them); a group with a NaN takes the scale's NaN code (255) with all codes
- * zero and reads back as NaN.
+ * -127.  (The conversion described with the format instead takes the exponent
+ * of amax, rounded down, and saturates: where amax's mantissa is above 1.5 its
+ * scale is half of this one.)  Non-finite values: a group with an infinity
+ * takes e = 127, so that it reads back as infinity (its finite elements keep
+ * what 2^127 leaves of them); a group with a NaN takes the scale's NaN code
+ * (255) with all codes zero and reads back as NaN.  The format itself has no
+ * infinity: the products below multiply such an element as the number
+ * 6 * 2^127, so that their results are infinite only where they leave the
+ * range of fp32 or bf16; a NaN stays NaN.
  *
  * Every MXFP4 call needs a row length that is a multiple of 32
  * (CDL_ERR_UNSUPPORTED otherwise), at most CDL_MAX_HIDDEN.
@@ -547,7 +552,8 @@ int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
 /*
  * cdl_grouped_mxfp4 -- each dispatched row times its expert's weights, both
  * MXFP4: out[r, n] = bf16_rne(sum_k a[r, k] * w[e, n, k]), e the row's
- * expert, accumulated in fp32.
+ * expert, accumulated in fp32.  Operands are the numbers that codes and scales
+ * stand for, those from 2^128 on (infinite when read back as bf16) too.
  *
  *   q, scales      in  [rows, K / 2] and [rows, K / 32] bytes
  *   w_q, w_scales  in  [L, N, K / 2] and [L, N, K / 32] bytes

@@ -7,7 +7,7 @@ import combine_dispatch_layout_amd as cdl
 import experts_check as C
 import experts_ref as R
 from gpu_util import DEV, announce, status_word
-from test_experts_gpu import gen, layer_inputs, mx_random, run_layer
+from test_experts_gpu import gen, layer_inputs, mx_random, run_layer, step
 
 pytestmark = pytest.mark.gpu
 
@@ -77,6 +77,76 @@ def test_grouped_forms_give_the_same_bits(K, N, swiglu):
     first = padded(256)
     for other in (padded(257), padded(700), segments(1, 0), segments(16, 3), segments(128, 500)):
         assert all(torch.equal(x, y) for x, y in zip(first, other))
+
+
+def test_grouped_infinite_and_nan_activations():
+    """MXFP4 has no infinity: a quantised one is the number 6 * 2^127, which the
+    products multiply as such (it is infinite where the product is, and read
+    back as bf16); the finite elements of its group are nothing beside it.  A
+    NaN stays NaN."""
+    announce("grouped, infinite activations")
+    K, N = 96, 64
+    x = torch.zeros(5, K, dtype=torch.bfloat16, device=DEV)
+    x[0, 5], x[1, 40], x[2, 70], x[3, 5] = torch.inf, -torch.inf, torch.nan, 2.0
+    x[0, 6] = 3.0                                      # of the infinity's group
+    q, s = cdl.quant_mxfp4(x)
+    assert torch.equal(cdl.dequant_mxfp4(q, s)[:2, [5, 40]], x[:2, [5, 40]])
+    wide = torch.zeros(1, N, K, dtype=torch.float64, device=DEV)
+    n = torch.arange(N, device=DEV)
+    wide[0, n, 5] = wide[0, n, 40] = torch.exp2(-(n // 2).double()) * torch.where(n % 2 == 1, -1.5, 1.0)
+    wide[0, :, 6] = 1.0 * wide[0, :, 5]
+    w = cdl.quant_mxfp4(wide.to(torch.bfloat16))
+    assert torch.equal(R.values(*w), wide)
+    out = cdl.grouped_mxfp4(q, s, *w, torch.tensor([5], dtype=torch.int32, device=DEV),
+                            torch.tensor([0, 5], device=DEV))
+    big = 6 * 2.0 ** 127 * wide[0, :, 5]
+    big = torch.where(big.abs() >= 2.0 ** 128, torch.sign(big) * torch.inf, big).to(torch.bfloat16)
+    assert int(torch.isfinite(big).sum()) > 50 and bool(torch.isinf(big).any())
+    assert torch.equal(out[0], big) and torch.equal(out[1], -big)
+    assert bool(torch.isnan(out[2]).all())
+    assert torch.equal(out[3], (2 * wide[0, :, 5]).to(torch.bfloat16)) and not bool(out[4].any())
+
+
+def test_swiglu_infinite_and_nan_values():
+    """h beyond fp32 is stored as +-6 * 2^127, as a quantised infinity is, h
+    with a NaN as NaN; the groups beside them are as without."""
+    announce("swiglu, infinite values")
+    K, I = 32, 96
+    x = torch.zeros(3, K, dtype=torch.bfloat16, device=DEV)
+    x[0, 0], x[1, 0], x[2, 0], x[2, 1] = 1.0, 1.0, 1.0, torch.nan
+    wide = torch.zeros(1, 2 * I, K, dtype=torch.bfloat16, device=DEV)
+    wide[0, :, 0] = 1.0
+    wide[0, [40, I + 40], 0] = 2.0 ** 66               # h = 2^132 in the second group
+    wide[0, [50, I + 50], 0] = torch.tensor([2.0 ** 66, -2.0 ** 66], dtype=torch.bfloat16, device=DEV)
+    q, s = cdl.grouped_swiglu_mxfp4(*cdl.quant_mxfp4(x), *cdl.quant_mxfp4(wide),
+                                    torch.tensor([3], dtype=torch.int32, device=DEV), torch.tensor([0, 3], device=DEV))
+    v = R.values(q, s)
+    one = 0.75                                         # of silu(1) = 0.731 at the scale 2^-3
+    want = torch.full((I,), one, dtype=torch.float64, device=DEV)
+    want[32:64] = 0.0
+    want[40], want[50] = 6 * 2.0 ** 127, -6 * 2.0 ** 127
+    assert torch.equal(v[0], want) and torch.equal(v[1], want)
+    assert bool(torch.isnan(v[2]).all())
+    back = cdl.dequant_mxfp4(q, s)
+    assert float(back[0, 40]) == torch.inf and float(back[0, 50]) == -torch.inf
+
+
+def test_expert_step_nonfinite_tokens_stay_apart():
+    """A token with a NaN gives NaN; one with an infinity, and one whose
+    activations overflow, leave every other token's row as it is."""
+    announce("expert step, non-finite tokens")
+    x, ids, wts, w13, w2 = layer_inputs(24, 256, 96, 4, 4, 2)
+    w13, w2 = cdl.quant_mxfp4(w13), cdl.quant_mxfp4(w2)
+    clean = step(x, ids, wts, w13, w2, 0, 1)[4]
+    x2 = x.clone()
+    x2[7, 5], x2[11, 9] = torch.nan, torch.inf
+    x2[13] = x2[13] * 2.0 ** 70
+    out = step(x2, ids, wts, w13, w2, 0, 1)[4]
+    keep = [t for t in range(24) if t not in (7, 11, 13)]
+    assert torch.equal(out[keep], clean[keep])
+    assert bool(torch.isnan(out[7]).all())
+    # sums of +-6 * 2^127 w: huge, infinite, or NaN where both signs overflow
+    assert not torch.equal(out[11], clean[11]) and not float(out[13].abs().max()) <= 2.0 ** 100
 
 
 FAR = (0, 31, 127, 128, 255, 256, 511, 4096, 131071, 131072, 200000, 262143)      # bytes of a row of 2^19 elements
