@@ -350,8 +350,8 @@ __device__ __forceinline__ void mx_layout_self(const PermuteArgs &a, int64_t blk
 // Layout and scatter in one launch (two with superblock counts): TPB row waves
 // quantise their tokens' rows while one more wave derives the workgroup's
 // destinations; after the one barrier the row waves store.  SELF: a small
-// batch, whose layout wave counts every slot itself, and whose rows are loaded
-// without first looking for a local slot.
+// batch, whose layout wave counts every slot itself; of up to 512 tokens (one a
+// workgroup) the rows are loaded without first looking for a local slot.
 template <int TPB, bool SELF, bool LL>
 __global__ __launch_bounds__((TPB + 1) * kWave) void mx_permute_kernel(PermuteArgs a, const uint16_t *__restrict__ x,
                                                                       int64_t H, uint8_t *__restrict__ oq,
@@ -374,11 +374,11 @@ __global__ __launch_bounds__((TPB + 1) * kWave) void mx_permute_kernel(PermuteAr
     } else if (real) {
         const rsrc_t r_tok = make_rsrc(a.ids + t * k, (uint32_t)k * 4u);
         id = buf_ld4(r_tok, (uint32_t)lane * 4u, 0);
-        row = SELF || __ballot(lane < k && local_expert(id, a.expert_begin, L) >= 0) != 0;
+        row = (SELF && TPB == 1) || __ballot(lane < k && local_expert(id, a.expert_begin, L) >= 0) != 0;
         if (row) held.load_quant(make_rsrc(x + t * H, (uint32_t)(H * 2)), lane, 0);
     }
     __syncthreads();
-    if (!row) return;
+    if (!(LL ? real : row)) return;            // (a padded form's map names every slot; without a row none is stored)
     int32_t d = lane < k ? dsts[wave * k + lane] : -1;
     bool drop = false;
     if constexpr (LL) {
@@ -1702,9 +1702,27 @@ int launch_mx_scatter(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
     return launch_status();
 }
 
-// Small batches (T * k <= 4096) lay themselves out in the launch that moves
-// their rows; one token a workgroup while there are few.
-constexpr int64_t kMxSelfSlots = 4096;
+// Small batches (at most 4096 slots) lay themselves out in the launch that
+// moves their rows; one token a workgroup up to 512 tokens, 4 above.  Every
+// workgroup then counts all slots and scans all experts, so that the layout's
+// own kernel and the scatter are the faster where slots, experts and workgroups
+// are many (few experts: the counting lanes also meet in the same words).
+// Measured, us for the one launch and for the two (H = 512):
+//   512 tokens of top-8: 11.1 and 9.2 (8 experts), 11.3 and 13.5 (128), 15.7
+//   and 14.5 (1024), 20.0 and 15.7 (2048); top-5, 8 experts: 8.6 and 9.2
+//   2048 experts: 128 tokens of top-4 13.6 and 18.9, of top-8 14.8 and 14.2,
+//   of top-32 24.0 and 34.8; 512 tokens of top-2 13.7 and 12.3
+//   1024 tokens, 32 of 256 experts: top-1 5.2 and 7.8, top-2 6.9 and 7.7,
+//   top-4 10.4 and 8.3; 4096 tokens of top-1 19.2 and 10.0
+//   1024 tokens of top-2: 128 experts 7.9 and 8.5, 512 experts 9.5 and 8.9
+inline bool mx_self_counting(int64_t T, int32_t k, int32_t L)
+{
+    const int64_t n = T * k;
+    if (T > 512) return n + 2 * L <= 2816;
+    if (n > 4096) return false;
+    if (L > 1024) return n <= 512 || k > 16;
+    return (L >= 64 && L <= 512) || T * n <= 3 << 19;
+}
 
 template <bool LL>
 int launch_mx_permute_self(const PermuteArgs &a, const uint16_t *x, int64_t H, uint8_t *q, uint8_t *s,
@@ -1729,9 +1747,11 @@ int launch_mx_permute_self(const PermuteArgs &a, const uint16_t *x, int64_t H, u
 // H = 7168, L = 128: 27.6 and 34.1 / 46.3 and 47.9 / 108.8 and 101.6;
 // H = 16384, 32 of 256 experts: 22.3 and 28.0 / 33.6 and 37.0 / 57.4 and 62.1
 // (16384 tokens: top-8 109 and 121, top-2 52 and 47; 32768, top-2: 114 and 83).
-inline bool mx_layout_apart(int64_t T, int64_t H)
+// Up to 4096 slots the layout is one kernel that counts them itself; those
+// batches take it where they do not lay themselves out above.
+inline bool mx_layout_apart(int64_t T, int32_t k, int64_t H)
 {
-    return T >= (H <= 4096 ? 4096 : H <= kMxPairs * 1024 ? 5121 : 16385);
+    return T * k <= 4096 || T >= (H <= 4096 ? 4096 : H <= kMxPairs * 1024 ? 5121 : 16385);
 }
 
 // Batches in between count their superblocks first.
@@ -1754,7 +1774,8 @@ int launch_mx_permute(PermuteArgs a, const uint16_t *x, int64_t H, uint8_t *q, u
     switch (p.tpb) {
     case 1: mx_permute_kernel<1, false, false><<<grid, dim3(2 * kWave), lds, stream>>>(a, x, H, q, s); break;
     case 2: mx_permute_kernel<2, false, false><<<grid, dim3(3 * kWave), lds, stream>>>(a, x, H, q, s); break;
-    default: mx_permute_kernel<4, false, false><<<grid, dim3(5 * kWave), lds, stream>>>(a, x, H, q, s); break;
+    case 4: mx_permute_kernel<4, false, false><<<grid, dim3(5 * kWave), lds, stream>>>(a, x, H, q, s); break;
+    default: return CDL_ERR_UNSUPPORTED;       // (8 tokens: only up to 4096 slots, which do not come here)
     }
     return launch_status();
 }
@@ -2002,8 +2023,8 @@ int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
                                 reorder_topk_ids, reorder_cap, status);
     a.cap_rows = cap_rows;
     if (T == 0) return run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
-    if (T * k <= kMxSelfSlots) return launch_mx_permute_self<false>(a, x, H, out_q, out_scales, (hipStream_t)stream);
-    if (mx_layout_apart(T, H)) {
+    if (mx_self_counting(T, k, L)) return launch_mx_permute_self<false>(a, x, H, out_q, out_scales, (hipStream_t)stream);
+    if (mx_layout_apart(T, k, H)) {
         rc = run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
         if (rc != CDL_OK) return rc;
         return launch_mx_scatter<false>(x, T, H, k, src2dst, out_q, out_scales, cap_rows, status, MxLL{},
@@ -2030,7 +2051,7 @@ int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, con
     if (!aligned(x, 16) || !aligned(out_q, 8)) return CDL_ERR_UNSUPPORTED;
     PermuteArgs a = layout_args(topk_ids, T, k, expert_begin, L, 1, counts, seg_indptr, src2dst, reorder_topk_ids,
                                 reorder_cap, status);
-    if (T > 0 && T * k <= kMxSelfSlots) {
+    if (T > 0 && mx_self_counting(T, k, L)) {
         a.ll_cap = cap;
         a.masked_m = masked_m;
         a.ll_src2dst = ll_src2dst;

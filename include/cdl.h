@@ -529,8 +529,8 @@ int cdl_dispatch_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const
 
 /*
  * cdl_permute_mxfp4 -- cdl_permute with MXFP4 rows, those of
- * cdl_dispatch_mxfp4.  One kernel launch for small batches (T*k <= 4096), two
- * otherwise.
+ * cdl_dispatch_mxfp4.  One kernel launch for small batches, two or three (the
+ * layout's own one or two, then the scatter) otherwise.
  */
 int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const int32_t *topk_ids,
                       int32_t expert_begin, int32_t L, int32_t alignment, int32_t *counts,

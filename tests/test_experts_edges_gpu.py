@@ -13,6 +13,52 @@ pytestmark = pytest.mark.gpu
 
 
 # ---------------------------------------------------------------------------
+# permutes
+# ---------------------------------------------------------------------------
+
+# both sides of the borders up to which a batch counts itself in the row launch
+BORDERS = [  # T, E, L, k
+    (512, 8, 8, 6), (512, 8, 8, 7), (511, 63, 63, 7), (511, 64, 64, 7), (512, 512, 512, 8), (400, 513, 513, 10),
+    (512, 1024, 1024, 6), (512, 1024, 1024, 7), (512, 1025, 1025, 1), (171, 1025, 1025, 3), (128, 1500, 1500, 4),
+    (129, 1500, 1500, 4), (100, 1100, 1100, 16), (100, 1100, 1100, 17), (513, 8, 8, 5), (513, 8, 8, 6), (2560, 256, 32, 1),
+    (2752, 256, 32, 1), (2753, 256, 32, 1), (1152, 256, 256, 2), (1153, 256, 256, 2), (2048, 32, 4, 2), (4096, 16, 4, 1),
+]
+
+
+@pytest.mark.parametrize("T,E,L,k", BORDERS)
+def test_permutes_at_the_self_counting_borders(T, E, L, k):
+    """The one-call permutes give the layout's own results and the rows that
+    the scatter from a given layout stores, tokens without a local slot among
+    them."""
+    announce("mxfp4 permutes T=%d E=%d L=%d k=%d" % (T, E, L, k))
+    H, b, A = 96, (E - L) // 2, 4
+    g = gen(T + E + k)
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, -1).indices.to(torch.int32)
+    ids[::5] = -1
+    x = torch.randn(T, H, generator=g, device=DEV).to(torch.bfloat16)
+    want = cdl.dispatch_layout(ids, b, L, alignment=A)
+    n, st = want.num_rows(), status_word()
+    q = torch.full((n + 3, H // 2), 0xA5, dtype=torch.uint8, device=DEV)
+    s = torch.full((n + 3, H // 32), 0xA5, dtype=torch.uint8, device=DEV)
+    q2, s2 = q.clone(), s.clone()
+    lay = cdl.permute_mxfp4(x, ids, b, L, out_q=q, out_scales=s, status=st, alignment=A)[0]
+    for f in ("counts", "seg_indptr", "src2dst", "reorder_topk_ids"):
+        assert torch.equal(getattr(lay, f), getattr(want, f)), f
+    cdl.dispatch_mxfp4(x, want, out_q=q2, out_scales=s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and int(st.item()) == 0
+    # padded, with room for all but the fullest experts' last rows
+    cap = max(1, int(want.counts.max()) - 1)
+    st0 = status_word()
+    _, _, mm0, map0 = cdl.permute_ll(x, ids, b, L, cap, status=st0)
+    _, ql, sl, mm, ll = cdl.permute_ll_mxfp4(x, ids, b, L, cap, status=st)
+    assert torch.equal(mm, mm0) and torch.equal(ll, map0) and torch.equal(st, st0)
+    kept = ll >= 0
+    rows, at = cdl.quant_mxfp4(x), torch.arange(T, device=DEV).repeat_interleave(k)[kept]
+    assert torch.equal(ql.view(L * cap, -1)[ll[kept].long()], rows[0][at])
+    assert torch.equal(sl.view(L * cap, -1)[ll[kept].long()], rows[1][at])
+
+
+# ---------------------------------------------------------------------------
 # grouped product
 # ---------------------------------------------------------------------------
 
