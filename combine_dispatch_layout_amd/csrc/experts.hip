@@ -1747,10 +1747,18 @@ int launch_mx_permute_self(const PermuteArgs &a, const uint16_t *x, int64_t H, u
 // H = 7168, L = 128: 27.6 and 34.1 / 46.3 and 47.9 / 108.8 and 101.6;
 // H = 16384, 32 of 256 experts: 22.3 and 28.0 / 33.6 and 37.0 / 57.4 and 62.1
 // (16384 tokens: top-8 109 and 121, top-2 52 and 47; 32768, top-2: 114 and 83).
+// Beyond 3 workgroups a CU (one launch of 704 of them: L = 2048, H = 512, top-8
+// 40.8 and 46.9; of 800: 59.5 and 51.3) many experts take the layout apart
+// earlier: 800 workgroups of top-8, L = 128: H = 512 24.5 and 22.9, H = 4096
+// 31.1 and 31.4; L = 512: H = 2048 36.8 and 35.3, H = 7168 51.2 and 55.8;
+// 1024 workgroups of top-8, H = 7168: L = 512 60.1 and 56.8, L = 2048 91.6 and
+// 76.9; of top-2, H = 512: L = 32 11.9 and 12.0, L = 2048 45.3 and 32.6.
 // Up to 4096 slots the layout is one kernel that counts them itself; those
 // batches take it where they do not lay themselves out above.
-inline bool mx_layout_apart(int64_t T, int32_t k, int64_t H)
+inline bool mx_layout_apart(int64_t T, int32_t k, int64_t H, int32_t L)
 {
+    const int64_t blocks = (T + kMaxTpbFp8 - 1) / kMaxTpbFp8;
+    if (blocks > 3 * 256 && L > (H <= 2048 ? 32 : H <= 4096 ? 128 : 512)) return true;
     return T * k <= 4096 || T >= (H <= 4096 ? 4096 : H <= kMxPairs * 1024 ? 5121 : 16385);
 }
 
@@ -2024,7 +2032,7 @@ int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
     a.cap_rows = cap_rows;
     if (T == 0) return run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
     if (mx_self_counting(T, k, L)) return launch_mx_permute_self<false>(a, x, H, out_q, out_scales, (hipStream_t)stream);
-    if (mx_layout_apart(T, k, H)) {
+    if (mx_layout_apart(T, k, H, L)) {
         rc = run_layout<kLayoutOnly>(a, ws, (hipStream_t)stream);
         if (rc != CDL_OK) return rc;
         return launch_mx_scatter<false>(x, T, H, k, src2dst, out_q, out_scales, cap_rows, status, MxLL{},

@@ -24,14 +24,20 @@ BORDERS = [  # T, E, L, k
     (2752, 256, 32, 1), (2753, 256, 32, 1), (1152, 256, 256, 2), (1153, 256, 256, 2), (2048, 32, 4, 2), (4096, 16, 4, 1),
 ]
 
+# and those from which the layout has kernels of its own: T, H, E, L, k
+APART = [
+    (3068, 2048, 33, 33, 2), (3080, 2048, 33, 33, 2), (3080, 2048, 32, 32, 2), (3080, 2080, 129, 129, 2),
+    (3080, 2080, 128, 128, 2), (3080, 4128, 513, 513, 2), (3080, 4128, 512, 512, 2), (4097, 32, 3, 3, 1),
+]
 
-@pytest.mark.parametrize("T,E,L,k", BORDERS)
-def test_permutes_at_the_self_counting_borders(T, E, L, k):
+
+@pytest.mark.parametrize("T,H,E,L,k", [(T, 96, E, L, k) for T, E, L, k in BORDERS] + APART)
+def test_permutes_at_the_borders_of_their_forms(T, H, E, L, k):
     """The one-call permutes give the layout's own results and the rows that
     the scatter from a given layout stores, tokens without a local slot among
     them."""
-    announce("mxfp4 permutes T=%d E=%d L=%d k=%d" % (T, E, L, k))
-    H, b, A = 96, (E - L) // 2, 4
+    announce("mxfp4 permutes T=%d H=%d E=%d L=%d k=%d" % (T, H, E, L, k))
+    b, A = (E - L) // 2, 4
     g = gen(T + E + k)
     ids = torch.rand(T, E, generator=g, device=DEV).topk(k, -1).indices.to(torch.int32)
     ids[::5] = -1
