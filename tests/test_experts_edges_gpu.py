@@ -333,3 +333,33 @@ def test_layer_smaller_batches_in_one_workspace(kind):
         out, v13, v2 = run_layer(kind, *a, 0, workspace=ws[:size])
         C.check_layer_output(out, *a[:3], v13, v2, 0)
         assert bool((ws[size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("T,H,I,E,L,k", [(1, 96, 64, 64, 64, 64), (2, 96, 64, 64, 64, 64), (2, 64, 544, 2048, 2048, 64),
+                                         (3, 4128, 32, 80, 70, 64), (64, 64, 96, 70, 64, 64), (128, 4128, 32, 40, 30, 32),
+                                         (2, 64, 32, 128, 1, 64), (128, 64, 288, 2, 2, 2)])
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+def test_layer_many_slots(T, H, I, E, L, k, kind):
+    """The most slots a token and a batch, and many of one expert, at both
+    ends of the batch."""
+    announce("layer %s T=%d H=%d I=%d E=%d L=%d k=%d" % (kind, T, H, I, E, L, k))
+    a = layer_inputs(T, H, I, E, L, k)
+    out, v13, v2 = run_layer(kind, *a, 0)
+    C.check_layer_output(out, *a[:3], v13, v2, 0)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("T,H,I", [(1, 96, 160), (2, 1056, 32), (5, 2592, 96), (40, 288, 544), (6, 16416, 32)])
+def test_layer_scales_at_any_byte(T, H, I, shift):
+    """Scale tensors that start at any byte between NaN codes."""
+    announce("layer, scales at byte %d, T=%d H=%d I=%d" % (shift, T, H, I))
+    x, ids, wts, w13, w2 = layer_inputs(T, H, I, 5, 4, 3)
+
+    def moved(s):
+        flat = torch.full((s.numel() + 8,), 255, dtype=torch.uint8, device=DEV)
+        flat[shift:shift + s.numel()] = s.flatten()
+        return flat[shift:shift + s.numel()].view(s.shape)
+
+    (q13, s13), (q2, s2) = cdl.quant_mxfp4(w13), cdl.quant_mxfp4(w2)
+    out = cdl.moe_layer_mxfp4(x, ids, wts, q13, moved(s13), q2, moved(s2))
+    C.check_layer_output(out, x, ids, wts, R.values(q13, s13), R.values(q2, s2), 0)
