@@ -540,7 +540,8 @@ int cdl_permute_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k, const 
 
 /*
  * cdl_permute_ll_mxfp4 -- cdl_permute_ll with MXFP4 rows: out_q
- * [L, cap, H / 2], out_scales [L, cap, H / 32].
+ * [L, cap, H / 2], out_scales [L, cap, H / 32].  One kernel launch for small
+ * batches, the layout's own and the scatter otherwise.
  */
 int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
                          const int32_t *topk_ids, int32_t expert_begin, int32_t L, int32_t *counts,
@@ -568,9 +569,10 @@ int cdl_permute_ll_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
  *                      the buffer is cut to what does and sets
  *                      CDL_STATUS_ROWS_OVERFLOW (segments) or
  *                      CDL_STATUS_LL_OVERFLOW (padded)
- * K % 32 == 0, q and w_q 16-byte aligned; any N >= 1.  CDL_ERR_TOO_LARGE
- * where L times the output tiles of one expert that owns the whole buffer (64
- * rows, 256 columns) exceeds 2^31 - 257.
+ * K % 32 == 0, q and w_q 16-byte aligned; any N from 1 to CDL_MAX_HIDDEN.
+ * CDL_ERR_TOO_LARGE where L times the output tiles of one expert that owns the
+ * whole buffer (64 or 256 rows, 256 columns) exceeds 2^31 - 257.  With a status
+ * word the counts are checked in a buffer of no rows too.
  */
 int cdl_grouped_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t K,
                       const uint8_t *w_q, const uint8_t *w_scales, int32_t L, int64_t N,
@@ -583,7 +585,8 @@ int cdl_grouped_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int
  * the I up rows of every expert, g and u the two products in fp32 and
  * h = g / (1 + exp(-g)) * u in fp32, the rows h are written as MXFP4:
  * out_q [rows, I / 2] (16-byte aligned), out_scales [rows, I / 32], the
- * input of the down product.  I % 32 == 0; the rest as cdl_grouped_mxfp4.
+ * input of the down product.  I % 32 == 0, I at most CDL_MAX_HIDDEN / 2, tiles
+ * of 128 columns; the rest as cdl_grouped_mxfp4.
  */
 int cdl_grouped_swiglu_mxfp4(const uint8_t *q, const uint8_t *scales, int64_t rows, int64_t K,
                              const uint8_t *w_q, const uint8_t *w_scales, int32_t L, int64_t I,
@@ -617,8 +620,8 @@ size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
  *   ws, ws_bytes      cdl_moe_layer_workspace_size bytes, 16-byte aligned, no
  *                     initialisation needed; calls that overlap need their own
  * T <= CDL_MOE_LAYER_MAX_TOKENS and T * k <= 4096 (CDL_ERR_UNSUPPORTED
- * otherwise: larger batches take the permute, the grouped products and the
- * combine); T * H and T' * k * I at most 2^31 - 9, T' = max(T, 2 min(T, 2))
+ * otherwise: larger batches of MXFP4 weights take the permute, the grouped
+ * products and the combine; this library has no grouped product of bf16 weights); T * H and T' * k * I at most 2^31 - 9, T' = max(T, 2 min(T, 2))
  * (CDL_ERR_TOO_LARGE); H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte
  * aligned, out 4-byte aligned.  The sums are taken in a fixed order: the
  * result is deterministic.
