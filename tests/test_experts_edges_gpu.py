@@ -7,7 +7,7 @@ import combine_dispatch_layout_amd as cdl
 import experts_check as C
 import experts_ref as R
 from gpu_util import DEV, announce, status_word
-from test_experts_gpu import gen, layer_inputs, mx_random, run_layer, step
+from test_experts_gpu import COUNTS, LAYERS, gen, layer_inputs, mx_random, run_layer, step
 
 pytestmark = pytest.mark.gpu
 
@@ -201,6 +201,36 @@ def test_expert_step_nonfinite_tokens_stay_apart():
     assert not torch.equal(out[11], clean[11]) and not float(out[13].abs().max()) <= 2.0 ** 100
 
 
+@pytest.mark.parametrize("counts,K,N", COUNTS)
+@pytest.mark.parametrize("form", ["segments", "padded"])
+def test_grouped_exact_sums(counts, K, N, form):
+    """Random codes at scales of 1 and 2: products are multiples of 2^-2 up to
+    144, sums of K < 29000 of them exact in fp32 in any order, results one
+    rounding to bf16 away."""
+    announce("grouped exact %s counts=%s K=%d N=%d" % (form, counts[:6], K, N))
+    assert K * 144 * 4 < 2 ** 24
+    g = gen(K + N + len(counts))
+    L = len(counts)
+    w, sw = mx_random(g, L, N, K, lo=127, hi=128)
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    if form == "padded":
+        cap, seg = max(counts) + 1, None
+        begins, shape = [e * cap for e in range(L)], (L, cap)
+    else:
+        begins = [sum(counts[:e]) + 3 * e for e in range(L)]
+        shape = (sum(counts) + 3 * L,)
+        seg = torch.tensor(begins + [shape[0]], device=DEV)
+    a, sa = mx_random(g, *shape, K, lo=127, hi=128)
+    out = torch.full((*shape, N), -7.5, dtype=torch.bfloat16, device=DEV)
+    cdl.grouped_mxfp4(a, sa, w, sw, c, seg, out=out)
+    a, sa, out = a.view(-1, K // 2), sa.view(-1, K // 32), out.view(-1, N)
+    want = torch.full_like(out, -7.5)
+    for e, n in enumerate(counts):
+        at = slice(begins[e], begins[e] + n)
+        want[at] = (R.values(a[at], sa[at]) @ R.values(w[e], sw[e]).t()).to(torch.bfloat16)
+    assert torch.equal(out, want)
+
+
 FAR = (0, 31, 127, 128, 255, 256, 511, 4096, 131071, 131072, 200000, 262143)      # bytes of a row of 2^19 elements
 
 
@@ -363,3 +393,57 @@ def test_layer_scales_at_any_byte(T, H, I, shift):
     (q13, s13), (q2, s2) = cdl.quant_mxfp4(w13), cdl.quant_mxfp4(w2)
     out = cdl.moe_layer_mxfp4(x, ids, wts, q13, moved(s13), q2, moved(s2))
     C.check_layer_output(out, x, ids, wts, R.values(q13, s13), R.values(q2, s2), 0)
+
+
+def exact_layer_inputs(T, H, I, E, L, k, b):
+    """Inputs of the layer whose every intermediate is exact, and its output in
+    64 bits.  x: n = 2^j ones at odd places, for the gates, and up to 16 of +-1
+    and +-2 at even ones; gate rows 32 / n or 64 / n at every odd place, so g is
+    32 or 64 and 1 + exp(-g) is 1 in fp32: silu(g) = g; up rows of -2 to 2 at
+    even places, so |u| <= 64 and h = g u is a bf16 number; down rows of -1 to
+    1, token weights 1, 1/2 and 1/4: sums are multiples of 8."""
+    g = gen(T * 7 + H + I + k)
+
+    def places(first, count):
+        """[T, count] distinct indices of the same parity."""
+        return torch.rand(T, H // 2, generator=g, device=DEV).topk(count, -1).indices * 2 + first
+
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, -1).indices.to(torch.int32)
+    wts = torch.exp2(-torch.randint(0, 3, (T, k), generator=g, device=DEV).float())
+    n = 1 << (min(32, H // 2).bit_length() - 1)
+    x = torch.zeros(T, H, device=DEV)
+    x.scatter_(1, places(1, n), torch.ones(T, n, device=DEV))
+    m = min(16, H // 2)
+    x.scatter_(1, places(0, m), torch.tensor([-2.0, -1.0, 1.0, 2.0], device=DEV)[
+        torch.randint(0, 4, (T, m), generator=g, device=DEV)])
+    w13 = torch.zeros(L, 2 * I, H, device=DEV)
+    w13[:, :I, 1::2] = torch.randint(1, 3, (L, I, 1), generator=g, device=DEV).float() * (32 / n)
+    w13[:, I:, 0::2] = torch.randint(-2, 3, (L, I, H // 2), generator=g, device=DEV).float()
+    w2 = torch.randint(-1, 2, (L, H, I), generator=g, device=DEV).float()
+    out = torch.zeros(T, H, dtype=torch.float64, device=DEV)
+    most = torch.zeros_like(out)
+    for e in range(L):
+        t, j = torch.nonzero(ids == e + b, as_tuple=True)
+        gu = x[t].double() @ w13[e].double().t()
+        assert bool(((gu[:, :I] == 32) | (gu[:, :I] == 64)).all())
+        h = gu[:, :I] * gu[:, I:]
+        assert torch.equal(h.to(torch.bfloat16).double(), h)
+        w = wts[t, j].double().unsqueeze(1)
+        out.index_add_(0, t, (h @ w2[e].double().t()) * w)
+        most.index_add_(0, t, (h.abs() @ w2[e].double().abs().t()) * w)
+    assert float(most.max()) < 8 * 2 ** 24                 # 24 bits of multiples of 8
+    return x.to(torch.bfloat16), ids, wts, w13.to(torch.bfloat16), w2.to(torch.bfloat16), out
+
+
+@pytest.mark.parametrize("T,H,I,E,L,k,b", LAYERS + [(1, 16416, 64, 4, 4, 2, 0), (2, 7168, 96, 32, 32, 8, 0),
+                                                   (128, 4128, 96, 40, 40, 4, 0), (64, 2048, 320, 16, 16, 8, 0)])
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4"])
+def test_layer_exact_sums(T, H, I, E, L, k, b, kind):
+    """Bounds of random sums grow with their depth; these sums are exact, so
+    that the output is one rounding to bf16 away, whatever the sizes."""
+    announce("layer exact %s T=%d H=%d I=%d E=%d L=%d k=%d" % (kind, T, H, I, E, L, k))
+    x, ids, wts, w13, w2, want = exact_layer_inputs(T, H, I, E, L, k, b)
+    out, v13, v2 = run_layer(kind, x, ids, wts, w13, w2, b)
+    assert torch.equal(v13, w13.double()) and torch.equal(v2, w2.double())
+    # (+ 0: a token without a slot gets +0)
+    assert torch.equal(out, want.to(torch.bfloat16) + 0)
