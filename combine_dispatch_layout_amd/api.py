@@ -146,6 +146,28 @@ def library():
         L.cdl_moe_layer.restype = ctypes.c_int
         L.cdl_moe_layer_mxfp4.argtypes = layer + [vp, vp, vp, vp, vp, vp, sz, vp]
         L.cdl_moe_layer_mxfp4.restype = ctypes.c_int
+        product = [vp, i64, i64, vp, i32, i64]
+        at = [vp, vp, i64]                       # counts, seg_indptr, cap
+        L.cdl_grouped_bf16.argtypes = product + at + [vp, vp, vp]
+        L.cdl_grouped_swiglu_bf16.argtypes = product + at + [vp, vp, vp]
+        L.cdl_grouped_swiglu_bf16_grad.argtypes = product + [vp] + at + [vp, vp, vp]
+        L.cdl_grouped_bf16_dx.argtypes = product + at + [vp, vp, vp]
+        L.cdl_grouped_bf16_dw.argtypes = [vp, vp, i64, i64, i64, i32] + at + [vp, vp, vp]
+        fp8 = [vp, vp, i32, i64, i64, vp, vp, i32, i64]
+        L.cdl_grouped_fp8.argtypes = fp8 + at + [vp, vp, vp]
+        L.cdl_grouped_swiglu_fp8.argtypes = fp8 + at + [vp, vp, vp, vp]
+        L.cdl_quant_fp8_blocks.argtypes = [vp, i64, i64, i64, vp, vp, vp]
+        L.cdl_dequant_fp8.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp]
+        L.cdl_rms_norm.argtypes = [vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, vp]
+        L.cdl_rms_norm_fp8.argtypes = [vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, i32, vp, vp, vp]
+        L.cdl_rms_norm_grad_workspace_size.argtypes = [i64, i64]
+        L.cdl_rms_norm_grad_workspace_size.restype = sz
+        L.cdl_rms_norm_grad.argtypes = [vp, vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, vp, sz, vp]
+        for name in ("cdl_grouped_bf16", "cdl_grouped_swiglu_bf16", "cdl_grouped_swiglu_bf16_grad",
+                     "cdl_grouped_bf16_dx", "cdl_grouped_bf16_dw", "cdl_grouped_fp8", "cdl_grouped_swiglu_fp8",
+                     "cdl_quant_fp8_blocks", "cdl_dequant_fp8", "cdl_rms_norm", "cdl_rms_norm_fp8",
+                     "cdl_rms_norm_grad"):
+            getattr(L, name).restype = ctypes.c_int
         L.cdl_ll_expected_m.argtypes = [i64, i32, i32, i32]
         L.cdl_ll_expected_m.restype = i64
         L.cdl_status_string.argtypes = [ctypes.c_int]
@@ -1015,3 +1037,349 @@ def moe_layer_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
             int(expert_begin), L, I, _ptr(w13_q), _ptr(w13_scales), _ptr(w2_q), _ptr(w2_scales), _ptr(out),
             _ptr(ws), ws.numel() * ws.element_size())
     return out
+
+
+# ---------------------------------------------------------------------------
+# products grouped by expert in bf16 and fp8
+# ---------------------------------------------------------------------------
+
+def _groups(rows: torch.Tensor, name: str, L: int, counts, seg_indptr, status):
+    """Checked rows of the grouped products, [rows, n] with seg_indptr and
+    [L, cap, n] without: (number of rows, cap)."""
+    _need(counts, "counts", torch.int32, (L,))
+    if seg_indptr is not None:
+        _need(seg_indptr, "seg_indptr", torch.int64, (L + 1,))
+        if rows.dim() != 2:
+            raise ValueError("%s must be [rows, n] with seg_indptr, got %s" % (name, tuple(rows.shape)))
+    elif rows.dim() != 3 or rows.shape[0] != L:
+        raise ValueError("%s must be [L, cap, n] with L = %d without seg_indptr, got %s" % (name, L, tuple(rows.shape)))
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(rows.device, counts=counts, seg_indptr=seg_indptr, status=status)
+    cap = 0 if seg_indptr is not None else rows.shape[1]
+    return (rows.shape[0] if seg_indptr is not None else L * cap), cap
+
+
+def _bf16_weights(w: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    _need(w, name, torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError("%s must be [L, N, K], got %s" % (name, tuple(w.shape)))
+    return tuple(w.shape)
+
+
+def _product_rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, width: int) -> torch.Tensor:
+    """bf16 rows [*like's rows, width] on its device: the given tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(*like.shape[:-1], width, dtype=torch.bfloat16, device=like.device)
+    _need(t, name, torch.bfloat16, (*like.shape[:-1], width))
+    return t
+
+
+def _bf16_product(what, x, w, counts, seg_indptr, out, status, width_of, extra=None):
+    _need(x, "x", torch.bfloat16)
+    L, N, K = _bf16_weights(w, "w")
+    if x.dim() < 2 or x.shape[-1] != K:
+        raise ValueError("x must have rows of K = %d elements, got %s" % (K, tuple(x.shape)))
+    rows, cap = _groups(x, "x", L, counts, seg_indptr, status)
+    n, width = width_of(N)
+    more = ()
+    if extra is not None:
+        _need(extra, "dh", torch.bfloat16, (*x.shape[:-1], n))
+        more = (_ptr(extra),)
+    out = _product_rows(out, "out", x, width)
+    _same_device(x.device, w=w, out=out, dh=extra)
+    _launch(what, x.device, _ptr(x), rows, K, _ptr(w), L, n, *more, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out),
+            _ptr(status))
+    return out
+
+
+def _halves(N: int) -> int:
+    if N % 2:
+        raise ValueError("w must hold as many gate as up rows, got %d rows" % N)
+    return N // 2
+
+
+def grouped_bf16(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg_indptr: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each row times its expert's weights w [L, N, K], in bf16 with fp32
+    accumulation.  With seg_indptr, x is [rows, K] and expert e owns the
+    counts[e] rows from seg_indptr[e]; without, x is the padded [L, cap, K]
+    buffer and counts its masked_m.  Rows of no expert are left as they were.
+    Returns out [rows, N] or [L, cap, N]."""
+    return _bf16_product("cdl_grouped_bf16", x, w, counts, seg_indptr, out, status, lambda N: (N, N))
+
+
+def grouped_swiglu_bf16(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor,
+                        seg_indptr: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gate/up product with SwiGLU in its epilogue: w [L, 2 I, K] holds the
+    I gate rows, then the I up rows.  Returns silu(gate) * up [rows, I] bf16,
+    the operand of the down product; the rest as grouped_bf16."""
+    return _bf16_product("cdl_grouped_swiglu_bf16", x, w, counts, seg_indptr, out, status,
+                         lambda N: (_halves(N), _halves(N)))
+
+
+def grouped_swiglu_bf16_grad(x: torch.Tensor, w: torch.Tensor, dh: torch.Tensor, counts: torch.Tensor,
+                             seg_indptr: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                             status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """From dh [rows, I], the gradient of grouped_swiglu_bf16's result, the
+    gradient of its gate and up values [rows, 2 I] (bf16): the dy of
+    grouped_bf16_dx and grouped_bf16_dw.  Gate and up are computed again from
+    x and w, so that the forward pass keeps neither."""
+    return _bf16_product("cdl_grouped_swiglu_bf16_grad", x, w, counts, seg_indptr, out, status,
+                         lambda N: (_halves(N), N), dh)
+
+
+def grouped_bf16_dx(dy: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg_indptr: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of grouped_bf16's rows: dy [rows, N] (or [L, cap, N]) times
+    w [L, N, K] as it lies.  Returns [rows, K]; rows of no expert are left as
+    they were."""
+    _need(dy, "dy", torch.bfloat16)
+    L, N, K = _bf16_weights(w, "w")
+    if dy.dim() < 2 or dy.shape[-1] != N:
+        raise ValueError("dy must have rows of N = %d elements, got %s" % (N, tuple(dy.shape)))
+    rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
+    out = _product_rows(out, "out", dy, K)
+    _same_device(dy.device, w=w, out=out)
+    _launch("cdl_grouped_bf16_dx", dy.device, _ptr(dy), rows, N, _ptr(w), L, K, _ptr(counts), _ptr(seg_indptr), cap,
+            _ptr(out), _ptr(status))
+    return out
+
+
+def grouped_bf16_dw(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, seg_indptr: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of grouped_bf16's weights: out[e] = the sum over e's rows of
+    dy[r, :, None] * x[r, None, :], [L, N, K] bf16; every element is written,
+    zeros for an expert without rows."""
+    _need(dy, "dy", torch.bfloat16)
+    _need(x, "x", torch.bfloat16)
+    if dy.dim() != x.dim() or dy.shape[:-1] != x.shape[:-1]:
+        raise ValueError("dy and x must have the same rows, got %s and %s" % (tuple(dy.shape), tuple(x.shape)))
+    L = counts.numel()
+    rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
+    N, K = dy.shape[-1], x.shape[-1]
+    if out is None:
+        out = torch.empty(L, N, K, dtype=torch.bfloat16, device=dy.device)
+    _need(out, "out", torch.bfloat16, (L, N, K))
+    _same_device(dy.device, x=x, out=out)
+    _launch("cdl_grouped_bf16_dw", dy.device, _ptr(dy), _ptr(x), rows, N, K, L, _ptr(counts), _ptr(seg_indptr), cap,
+            _ptr(out), _ptr(status))
+    return out
+
+
+def _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status):
+    _need(q, "q", torch.uint8)
+    _need(w_q, "w_q", torch.uint8)
+    if w_q.dim() != 3:
+        raise ValueError("w_q must be [L, N, K], got %s" % (tuple(w_q.shape),))
+    L, N, K = w_q.shape
+    if K % FP8_GROUP:
+        raise CdlError(-3, "fp8 product (K must be a multiple of %d)" % FP8_GROUP)
+    if q.dim() < 2 or q.shape[-1] != K:
+        raise ValueError("q must have rows of K = %d bytes, got %s" % (K, tuple(q.shape)))
+    _need(w_scales, "w_scales", torch.float32, (L, -(-N // FP8_GROUP), K // FP8_GROUP))
+    rows, cap = _groups(q, "q", L, counts, seg_indptr, status)
+    _check_scale_buffer(scales, rows, K, scale_flags, cap if seg_indptr is None else rows)
+    _same_device(q.device, scales=scales, w_q=w_q, w_scales=w_scales)
+    return L, N, K, rows, cap
+
+
+def grouped_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor, counts: torch.Tensor,
+                seg_indptr: Optional[torch.Tensor] = None, scale_flags: int = 0, out: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each fp8 row times its expert's fp8 weights, in bf16 with fp32
+    accumulation: q and scales as the fp8 dispatches write them (any
+    scale_flags format), w_q [L, N, K] and w_scales [L, ceil(N / 128), K / 128]
+    as quant_fp8_blocks does.  Rows and counts as for grouped_bf16."""
+    L, N, K, rows, cap = _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status)
+    out = _product_rows(out, "out", q, N)
+    _same_device(q.device, out=out)
+    _launch("cdl_grouped_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, K, _ptr(w_q), _ptr(w_scales), L, N,
+            _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status))
+    return out
+
+
+def grouped_swiglu_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor,
+                       counts: torch.Tensor, seg_indptr: Optional[torch.Tensor] = None, scale_flags: int = 0,
+                       out_q: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gate/up product with SwiGLU, quantised again in its epilogue: w_q
+    [L, 2 I, K] holds the I gate rows, then the I up rows.  Returns (q
+    [rows, I], scales in the input's scale_flags format), the operand of the
+    down product."""
+    L, N, K, rows, cap = _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status)
+    I = _halves(N)
+    if I % FP8_GROUP:
+        raise CdlError(-3, "grouped_swiglu_fp8 (I must be a multiple of %d)" % FP8_GROUP)
+    if out_q is None:
+        out_q = torch.empty(*q.shape[:-1], I, dtype=torch.uint8, device=q.device)
+    _need(out_q, "out_q", torch.uint8, (*q.shape[:-1], I))
+    rpm = cap if seg_indptr is None else rows
+    if out_scales is None:
+        out_scales = _new_scales(q.shape[:-1], I, scale_flags, q.device, rpm)
+    _check_scale_buffer(out_scales, rows, I, scale_flags, rpm)
+    _same_device(q.device, out_q=out_q, out_scales=out_scales)
+    _launch("cdl_grouped_swiglu_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, K, _ptr(w_q), _ptr(w_scales),
+            L, I, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out_q), _ptr(out_scales), _ptr(status))
+    return out_q, out_scales
+
+
+def _new_scales(lead, H: int, scale_flags: int, device, rows_per_mat: int) -> torch.Tensor:
+    """A scale buffer for rows [*lead, H], shaped as the dispatches shape theirs."""
+    rows = 1
+    for n in lead:
+        rows *= n
+    t = new_scale_tensor(rows, H, scale_flags, device, rows_per_mat)
+    return t if scale_flags & FP8_SCALE_COLMAJOR else t.view(*lead, t.shape[-1])
+
+
+def quant_fp8_blocks(w: torch.Tensor, out_q: Optional[torch.Tensor] = None,
+                     out_scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """bf16 weights w [..., N, K] to fp8 (e4m3fn) with one fp32 scale, amax /
+    448, for each block of 128 x 128: (q [..., N, K] uint8, scales
+    [..., ceil(N / 128), K / 128])."""
+    _need(w, "w", torch.bfloat16)
+    if w.dim() < 2:
+        raise ValueError("w must be [..., N, K]")
+    N, K = w.shape[-2:]
+    if K < 1 or K % FP8_GROUP:
+        raise CdlError(-3, "quant_fp8_blocks (K must be a multiple of %d)" % FP8_GROUP)
+    lead = w.shape[:-2]
+    if out_q is None:
+        out_q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    if out_scales is None:
+        out_scales = torch.empty(*lead, -(-N // FP8_GROUP), K // FP8_GROUP, dtype=torch.float32, device=w.device)
+    _need(out_q, "out_q", torch.uint8, w.shape)
+    _need(out_scales, "out_scales", torch.float32, (*lead, -(-N // FP8_GROUP), K // FP8_GROUP))
+    _same_device(w.device, out_q=out_q, out_scales=out_scales)
+    mats = 1
+    for n in lead:
+        mats *= n
+    _launch("cdl_quant_fp8_blocks", w.device, _ptr(w), mats, N, K, _ptr(out_q), _ptr(out_scales))
+    return out_q, out_scales
+
+
+def dequant_fp8(q: torch.Tensor, scales: torch.Tensor, scale_flags: int = 0,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fp8 rows q [rows, H] (or the padded [L, cap, H]) and their scales in any
+    scale_flags format as bf16 rows: the product of code and scale in fp32,
+    rounded once."""
+    _need(q, "q", torch.uint8)
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [rows, H] or [L, cap, H], got %s" % (tuple(q.shape),))
+    H = q.shape[-1]
+    if H < 1 or H % FP8_GROUP:
+        raise CdlError(-3, "dequant_fp8 (H must be a multiple of %d)" % FP8_GROUP)
+    rows = q.numel() // H
+    rpm = q.shape[-2]
+    _check_scale_buffer(scales, rows, H, scale_flags, rpm)
+    out = _product_rows(out, "out", q, H)
+    _same_device(q.device, scales=scales, out=out)
+    _launch("cdl_dequant_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, H, rpm, _ptr(out))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------
+
+def _norm_args(x, weight, eps, **others):
+    """Checked bf16 rows x [..., H] and weight [H]: (T, H)."""
+    _need(x, "x", torch.bfloat16)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., H]")
+    H = x.shape[-1]
+    _need(weight, "weight", torch.bfloat16, (H,))
+    if not eps >= 0:
+        raise ValueError("eps must be >= 0, got %r" % (eps,))
+    _same_device(x.device, weight=weight, **others)
+    return x.numel() // H, H
+
+
+def _same_rows(t: Optional[torch.Tensor], name: str, x: torch.Tensor) -> torch.Tensor:
+    return _product_rows(t, name, x, x.shape[-1])
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
+    """The norm before a layer: out = h / sqrt(mean(h^2) + eps) * weight over
+    rows [..., H] of bf16, in fp32 and rounded once.  With residual, h is
+    x + residual rounded to bf16 (what the residual path keeps is what is
+    normed); then returns (out, h), otherwise out.  out and residual_out may be
+    x or residual itself."""
+    T, H = _norm_args(x, weight, eps, residual=residual, out=out, residual_out=residual_out)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, x.shape)
+        residual_out = _same_rows(residual_out, "residual_out", x)
+    out = _same_rows(out, "out", x)
+    _launch("cdl_rms_norm", x.device, _ptr(x), _ptr(residual), _ptr(weight), float(eps), T, H, _ptr(out),
+            _ptr(residual_out))
+    return out if residual is None else (out, residual_out)
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 scale_flags: int = 0, out_q: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
+    """rms_norm of rows x [T, H] with its fp32 result quantised in groups of
+    128 as the fp8 dispatch quantises rows (amax / 448, or the formats of
+    scale_flags).  Returns (q [T, H] uint8, scales) and with residual also h;
+    `out`, where given, receives the bf16 rows as well (a router's input)."""
+    T, H = _norm_args(x, weight, eps, residual=residual, out=out, residual_out=residual_out)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    if H % FP8_GROUP:
+        raise CdlError(-3, "rms_norm_fp8 (H must be a multiple of %d)" % FP8_GROUP)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, x.shape)
+        residual_out = _same_rows(residual_out, "residual_out", x)
+    if out is not None:
+        out = _same_rows(out, "out", x)
+    if out_q is None:
+        out_q = torch.empty(T, H, dtype=torch.uint8, device=x.device)
+    _need(out_q, "out_q", torch.uint8, (T, H))
+    if out_scales is None:
+        out_scales = new_scale_tensor(T, H, scale_flags, x.device)
+    _check_scale_buffer(out_scales, T, H, scale_flags, T)
+    _same_device(x.device, out_q=out_q, out_scales=out_scales)
+    _launch("cdl_rms_norm_fp8", x.device, _ptr(x), _ptr(residual), _ptr(weight), float(eps), T, H, _ptr(out_q),
+            _ptr(out_scales), int(scale_flags), _ptr(out), _ptr(residual_out))
+    return (out_q, out_scales) if residual is None else (out_q, out_scales, residual_out)
+
+
+def rms_norm_grad_workspace_size(T: int, H: int) -> int:
+    n = library().cdl_rms_norm_grad_workspace_size(T, H)
+    if n == 0:
+        raise CdlError(-2, "cdl_rms_norm_grad_workspace_size")
+    return int(n)
+
+
+def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                  dresidual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  dweight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The gradient of rms_norm: dy and the normed rows h (x, or the sum that
+    rms_norm returned) [..., H] give (dx [..., H] bf16, dweight [H] fp32).  dx is
+    the gradient of h, so of x and of residual alike; dresidual, the gradient
+    that reaches h past the norm, is added to it before the one rounding.  out
+    may be dy, h or dresidual itself.  Deterministic."""
+    T, H = _norm_args(h, weight, eps, dy=dy, dresidual=dresidual, out=out, dweight=dweight, workspace=workspace)
+    _need(dy, "dy", torch.bfloat16, h.shape)
+    if dresidual is not None:
+        _need(dresidual, "dresidual", torch.bfloat16, h.shape)
+    out = _same_rows(out, "out", h)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=torch.float32, device=h.device)
+    _need(dweight, "dweight", torch.float32, (H,))
+    need = rms_norm_grad_workspace_size(T, H)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
+    _need_gpu(workspace, "workspace")
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace too small: need %d bytes" % need)
+    _launch("cdl_rms_norm_grad", h.device, _ptr(dy), _ptr(h), _ptr(weight), _ptr(dresidual), float(eps), T, H, _ptr(out),
+            _ptr(dweight), _ptr(workspace), workspace.numel() * workspace.element_size())
+    return out, dweight

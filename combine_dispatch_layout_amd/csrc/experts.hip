@@ -420,7 +420,8 @@ struct GroupedArgs {
 
 // Expert e's first row and its row count, held inside the buffer whatever
 // the device arrays say.
-__device__ __forceinline__ int64_t grouped_rows(const GroupedArgs &a, int e, int64_t *begin, bool *bad)
+template <typename Args>
+__device__ __forceinline__ int64_t grouped_rows(const Args &a, int e, int64_t *begin, bool *bad)
 {
     int64_t c = a.counts[e], b = a.seg ? a.seg[e] : (int64_t)e * a.cap;
     const int64_t most = a.seg ? a.rows : a.cap;
@@ -445,8 +446,8 @@ struct GroupedTile {
 // The number of tiles before the end of every expert, into LDS (ends[L]);
 // returns all of them.  Every wave scans, wave 0 writes; the caller
 // synchronises.
-template <int MT>
-__device__ __forceinline__ int32_t grouped_tile_table(const GroupedArgs &a, int tiles_n, int32_t *ends)
+template <int MT, typename Args>
+__device__ __forceinline__ int32_t grouped_tile_table(const Args &a, int tiles_n, int32_t *ends)
 {
     const int lane = threadIdx.x & (kWave - 1);
     int32_t base = 0;
@@ -471,7 +472,8 @@ __device__ __forceinline__ int32_t grouped_tile_table(const GroupedArgs &a, int 
 // Tile `id` of the table: tiles are ordered by expert, then column tile, then
 // row tile (the row tiles of one weight tile run side by side, so its second
 // reader finds it in a cache).
-__device__ __forceinline__ GroupedTile grouped_tile(const GroupedArgs &a, const int32_t *ends, int tiles_n, int32_t id)
+template <typename Args>
+__device__ __forceinline__ GroupedTile grouped_tile(const Args &a, const int32_t *ends, int tiles_n, int32_t id)
 {
     const int lane = threadIdx.x & (kWave - 1);
     GroupedTile t;

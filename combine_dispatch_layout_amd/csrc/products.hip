@@ -1,0 +1,998 @@
+// products.hip -- the products grouped by expert in bf16 and in fp8 (e4m3fn
+// rows with a scale per 128 elements, weights with one per 128 x 128 block),
+// their SwiGLU forms and the bf16 gradients, for MI355X (gfx950).  Included
+// after experts.hip (same translation unit).
+
+namespace {
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// One kernel for all of them: out[b, a] = sum over the depth of A[a] * B[b],
+// an output column a and an output row b.
+//
+//   form  A (256 of a tile)        B (MT of a tile)          depth
+//   kFwd  rows of W[e] (n)         token rows                K
+//   kDx   columns of W[e] (k)      rows of dy                N
+//   kDw   columns of x (k)         columns of dy (n)         the expert's rows
+//
+// Depth runs along a row's bytes for operands taken by rows and across rows
+// for those taken by columns.
+// ---------------------------------------------------------------------------
+// The scale and codes of a group of 128 values in fp8 from its largest
+// magnitude (over its values that are not NaN; infinite if one is): the
+// dispatch's quantisation, of 32-bit values.
+struct Fp8Group {
+    float scale;
+    int ex;                      // UE8M0: scale = 2^ex
+    bool ue8m0, empty;
+
+    __device__ __forceinline__ Fp8Group(float amax, bool ue) : ex(-127), ue8m0(ue), empty(!(amax > 0.0f))
+    {
+        if (ue8m0) {
+            if (!empty) {
+                int x = 0;
+                const float m = frexpf(amax, &x);            // 448 = 0.875 * 2^9
+                ex = amax == __builtin_huge_valf() ? 127 : x - 9 + (m > 0.875f ? 1 : 0);
+                ex = ex < -127 ? -127 : ex;
+            }
+            scale = ldexpf(1.0f, ex);
+        } else {
+            scale = amax / 448.0f;                           // correctly rounded
+        }
+    }
+    __device__ __forceinline__ uint8_t exponent() const { return (uint8_t)(ex + 127); }
+    __device__ __forceinline__ float quotient(float x) const
+    {
+        if (ue8m0) return ldexpf(x, -ex);
+        const float d = empty ? x : x / scale;               // correctly rounded
+        return d > 448.0f ? 448.0f : d < -448.0f ? -448.0f : d;
+    }
+    // a NaN quotient (or an infinite one, of a power of two) takes the NaN code with x's sign
+    __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) const
+    {
+        const float x[4] = {a, b, c, d};
+        float q[4];
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[i] = quotient(x[i]);
+            odd |= !__builtin_isfinite(q[i]);
+        }
+        if (!odd) return pack4_e4m3(q[0], q[1], q[2], q[3]);
+        uint32_t r = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool fin = __builtin_isfinite(q[i]);
+            const uint32_t code = fin ? pack2_e4m3(q[i], 0.0f) & 0xFFu : (__float_as_uint(x[i]) >> 24 & 0x80u) | 0x7Fu;
+            r |= code << (8 * i);
+        }
+        return r;
+    }
+};
+
+enum ProductForm { kFwd, kDx, kDw };
+enum ProductEpilogue { kPlain, kSwiglu, kSwigluGrad };
+
+struct ProductArgs {
+    const uint8_t *a;
+    const uint8_t *b;
+    int64_t rows;                // token rows of the buffer
+    int64_t K, N;                // weights [L, N, K] (SwiGLU: N = 2 I)
+    int32_t L;
+    const int32_t *counts;
+    const int64_t *seg;          // NULL: expert e's rows start at e * cap
+    int64_t cap;
+    int32_t *status;
+    uint16_t *out;
+    const uint16_t *dh;          // SwiGLU gradient: [rows, I]
+    // fp8
+    const uint8_t *b_s;          // token scales in the format below
+    const float *a_s;            // [L, ceil(N / 128), K / 128]
+    int64_t s_row, s_batch;      // words from a row's scales to the next row's, to the next four groups'
+    int64_t s_group;             // column-major fp32: words to the next group's; else 0
+    int64_t s_mat;               // column-major, padded: words of one expert's matrix; else 0
+    int32_t s_packed;            // exponent bytes, four groups a word
+    int32_t s_flags;
+    uint8_t *hq;                 // SwiGLU: [rows, I] e4m3fn and its scales in the same format
+    void *hs;
+    int64_t h_row, h_group, h_mat;   // words of hs: row to row, word of groups to word, expert's matrix to the next
+};
+
+constexpr int kProductThreads = 512;
+constexpr int kProductNT = 256;          // A of a tile
+constexpr int kProductWgs = 256;         // one per CU
+constexpr int kLine = 128;               // bytes of a row per stage: 64 bf16, or the 128 elements of an fp8 scale
+constexpr int kScaleRing = 4;            // batches (four stages' scales) in LDS
+constexpr uint32_t kFar = 0x80000000u;   // no tile operand reaches this offset: loads there read no memory and give zeros
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p;
+}
+
+// Loads that go to LDS directly, lane l's 16 (4) bytes to `to` + 16 (4) * l.
+// In assembly, because the compiler cannot tell the buffers of a ring apart and
+// waits for every such load before any read of LDS; these are waited for with
+// sync_stage().  They have no register output, and lanes out of range write
+// zeros.  M0 holds the LDS address; nothing else here uses it.
+__device__ __forceinline__ void dma16(u32x4 r, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(to));
+}
+__device__ __forceinline__ void dma4(u32x4 r, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(to));
+}
+// (the values are the same in all lanes)
+__device__ __forceinline__ u32x4 scalar_rsrc(const uint8_t *base, uint32_t bytes)
+{
+    const uint64_t p = (uint64_t)base;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xFFFFu)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)kRsrcWord3};
+}
+
+// All but the wave's newest LEFT loads have arrived, its reads of LDS too, and
+// so have every other wave's.
+template <int LEFT>
+__device__ __forceinline__ void sync_stage()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ void swap_rows16(uint32_t &a, uint32_t &b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+template <bool FP8, ProductForm FORM, int MT>
+struct ProductShape {
+    static constexpr int WN = MT == 256 ? 2 : 4;
+    // wave w has A part w % WN and B part w / WN: the two waves of a SIMD
+    // (w, w + 4) are in different halves of B, so a tile that is half full keeps
+    // every SIMD busy
+    static constexpr int WM = 8 / WN;
+    static constexpr int NF = kProductNT / 16 / WN;      // 16-row fragments per wave
+    static constexpr int MF = MT / 16 / WM;
+    static constexpr bool kACols = FORM != kFwd, kBCols = FORM == kDw;
+    static constexpr int kBufs = MT == 256 ? 2 : 3;
+    static constexpr int kBuf = (kProductNT + MT) * kLine;
+    static constexpr int kAUnits = 4, kBUnits = MT / 64; // loads per wave and stage
+    static constexpr int kScaleBatch = MT * 16 + 1024;   // token scales, then the weights'
+    static constexpr int kScales = kBufs * kBuf;
+    static constexpr int kAmax = kScales + (FP8 ? kScaleRing * kScaleBatch : 0);
+    static constexpr size_t kLds = kAmax + (FP8 ? WN * MT * 4 : 0);   // then the tile table
+};
+
+// What one side of a tile loads in a stage.
+struct ProductSide {
+    const uint8_t *p;            // by rows: the tile's first row; by columns: depth row 0
+    const uint8_t *p2;           // SwiGLU: the first up row
+    uint32_t bytes;              // by rows: bytes of the tile's rows
+    int64_t depth;               // by columns: rows
+    uint32_t ld;                 // bytes of a row
+    uint32_t off;                // the lane's offset in unit 0 of stage 0
+};
+
+template <bool FP8, ProductForm FORM, ProductEpilogue EPI, int MT>
+struct ProductWg {
+    using S = ProductShape<FP8, FORM, MT>;
+    static constexpr int kCols = EPI == kPlain ? kProductNT : kProductNT / 2;     // output columns of a tile
+    static constexpr int NF = S::NF, MF = S::MF;
+    static constexpr int R = 2, D = R - 1;                     // fragments of A in registers, read ahead
+    static constexpr bool kUpByUnit = EPI != kPlain && S::WN == 2, kUpByHalf = EPI != kPlain && S::WN == 4;
+
+    const ProductArgs a;
+    uint8_t *const lds;
+    const int tid, lane, wave, wn, wm;
+    const uint32_t lds0;                     // LDS address of the buffers
+    // operands being loaded
+    ProductSide sa, sb;
+    int load_stage, load_stages;
+    const uint8_t *tok_s, *w_s;              // fp8: the tile's scales
+    int live_rows, live_blocks;              // rows with scales; weight scale blocks
+    uint32_t load_batch, batch;              // ring positions
+    // the tile being multiplied
+    int64_t row0, n0, begin;
+    int live_m, live_n, e, stages;
+    int64_t next_row0, next_n0, next_begin;
+    int next_live_m, next_live_n, next_e, next_stages;
+
+    f32x4 acc[NF][MF];
+    i32x8 fa[R], fb[MF];
+
+    __device__ __forceinline__ ProductWg(const ProductArgs &args, uint8_t *l)
+        : a(args), lds(l), tid(threadIdx.x), lane(tid & (kWave - 1)), wave(wave_id()), wn(wave % S::WN), wm(wave / S::WN),
+          lds0(lds_address(l)), load_batch(0), batch(0)
+    {
+    }
+
+    // ---- loading ----
+
+    // A lane's offset in unit 0: by rows, 8 lanes take the 128 bytes of a row,
+    // 16-byte chunk c of row r going to chunk c ^ (r / 2 % 8), so that the
+    // fragment reads (16 rows, one chunk) touch all 64 banks; by columns, 32
+    // lanes take 512 bytes of a depth row, 32-byte block c of depth row d going
+    // to block c ^ (d % 4 + 4 (d / 8 % 2)), so that the transposing reads of 32
+    // lanes (8 depth rows, 32 bytes each) do.  Unit j is 64 LDS rows (16 depth
+    // rows) further on, which leaves these unchanged.
+    __device__ __forceinline__ uint32_t row_chunk() const { return (uint32_t)((lane & 7) ^ (((wave & 1) << 2 | lane >> 4) & 7)); }
+    __device__ __forceinline__ uint32_t column_chunk() const
+    {
+        const int d = 2 * wave + (lane >> 5);
+        return (uint32_t)((lane & 31) ^ (((d & 3) | (d >> 3 & 1) << 2) << 1));
+    }
+
+    __device__ __forceinline__ void side_by_rows(ProductSide &s, const uint8_t *p, int64_t ld, int live, int half_rows)
+    {
+        s.p = p;
+        s.ld = (uint32_t)ld;
+        s.bytes = (uint32_t)live * s.ld;
+        s.off = (uint32_t)((half_rows ? (wave & 3) : wave) * 8 + (lane >> 3)) * s.ld + row_chunk() * 16;
+    }
+    __device__ __forceinline__ void side_by_columns(ProductSide &s, const uint8_t *p, int64_t ld, int64_t depth, int64_t first)
+    {
+        s.p = p;
+        s.ld = (uint32_t)ld;
+        s.depth = depth;
+        const uint32_t at = (uint32_t)first * 2 + column_chunk() * 16;
+        s.off = at < s.ld ? (uint32_t)(2 * wave + (lane >> 5)) * s.ld + at : kFar;
+    }
+
+    // Stage s of a side to LDS address `to`.
+    template <int UNITS, bool COLS, bool IS_A>
+    __device__ __forceinline__ void load_side(const ProductSide &s, int stage, uint32_t to) const
+    {
+        if constexpr (COLS) {
+            const int64_t d0 = (int64_t)stage * 64;
+            const int64_t left = s.depth - d0;
+            const u32x4 r = scalar_rsrc(s.p + d0 * s.ld, (uint32_t)(left <= 0 ? 0 : left < 64 ? left : 64) * s.ld);
+            uint32_t off = s.off;
+#pragma unroll
+            for (int j = 0; j < UNITS; ++j, off += 16 * s.ld) dma16(r, off, to + wave * 1024 + j * 8192);
+        } else {
+            const uint32_t k = (uint32_t)stage * kLine;
+            uint32_t off = k + row_chunk() * 16 < s.ld ? s.off + k : kFar;
+            const u32x4 r = scalar_rsrc(s.p, s.bytes);
+            if constexpr (IS_A && kUpByUnit) {
+                const u32x4 r2 = scalar_rsrc(s.p2, s.bytes);
+#pragma unroll
+                for (int j = 0; j < UNITS; ++j) {
+                    dma16(j & 1 ? r2 : r, off, to + wave * 1024 + j * 8192);
+                    if (j & 1) off += 64 * s.ld;
+                }
+            } else {
+                const u32x4 rr = IS_A && kUpByHalf && wave >= 4 ? scalar_rsrc(s.p2, s.bytes) : r;
+#pragma unroll
+                for (int j = 0; j < UNITS; ++j, off += (IS_A && kUpByHalf ? 32 : 64) * s.ld)
+                    dma16(rr, off, to + wave * 1024 + j * 8192);
+            }
+        }
+    }
+
+    // The scales of stages 4 q to 4 q + 3: a row's four words (or the word that
+    // packs them) per lane, the weights' by wave 7.
+    __device__ __forceinline__ void load_scales(int q)
+    {
+        const uint32_t to = lds0 + S::kScales + (load_batch % kScaleRing) * S::kScaleBatch;
+        if (wave < MT / 64) {
+            const int row = wave * 64 + lane;
+            const uint8_t *p = tok_s + (int64_t)q * a.s_batch * 4;
+            if (a.s_row == 1) {
+                const u32x4 r0 = scalar_rsrc(p, (uint32_t)live_rows * 4);
+                dma4(r0, (uint32_t)row * 4, to + wave * 256);
+                if (a.s_group) {
+                    const int64_t left = a.K / 128 - 4 * q;
+#pragma unroll
+                    for (int g = 1; g < 4; ++g)
+                        dma4(scalar_rsrc(p + g * a.s_group * 4, left > g ? (uint32_t)live_rows * 4 : 0u), (uint32_t)row * 4,
+                             to + g * (MT * 4) + wave * 256);
+                }
+            } else {
+                const u32x4 r = scalar_rsrc(p, (uint32_t)live_rows > 0 ? (uint32_t)(live_rows * a.s_row - q * a.s_batch) * 4 : 0u);
+                if (a.s_packed)
+                    dma4(r, (uint32_t)row * (uint32_t)a.s_row * 4, to + wave * 256);
+                else
+                    dma16(r, (uint32_t)row * (uint32_t)a.s_row * 4, to + wave * 1024);
+            }
+        } else if (wave == 7) {
+            const int64_t G = a.K / 128;
+            const uint32_t step = (uint32_t)(EPI == kPlain ? G : a.N / 256 * G) * 4;
+            const uint32_t bytes = live_blocks == 0 ? 0u : (uint32_t)((live_blocks - 1) * (int64_t)step + G * 4) - (uint32_t)q * 16;
+            dma16(scalar_rsrc(w_s + (int64_t)q * 16, bytes), lane < 2 ? (uint32_t)lane * step : kFar, to + MT * 16);
+        }
+        ++load_batch;
+    }
+
+    // The next stage in order to buffer `buf`; next() moves to the next tile.
+    template <typename F>
+    __device__ __forceinline__ void load_next(int buf, F &&next)
+    {
+        if (load_stage == load_stages) {
+            next();
+            load_stage = 0;
+        }
+        if (FP8 && (load_stage & 3) == 0) load_scales(load_stage >> 2);
+        const uint32_t to = lds0 + (uint32_t)buf * S::kBuf;
+        load_side<S::kAUnits, S::kACols, true>(sa, load_stage, to);
+        load_side<S::kBUnits, S::kBCols, false>(sb, load_stage, to + kProductNT * kLine);
+        ++load_stage;
+    }
+
+    // Sets what is loaded to tile `id`.
+    __device__ __forceinline__ void set_tile(const GroupedTile &t)
+    {
+        const int64_t eb = FP8 ? 1 : 2;
+        next_e = t.e;
+        next_begin = t.begin;
+        next_n0 = (int64_t)t.n * kCols;
+        if constexpr (FORM == kDw) {
+            next_row0 = (int64_t)t.m * MT;                   // a row of the weights
+            next_live_m = (int)(a.N - next_row0 < MT ? a.N - next_row0 : MT);
+            next_live_n = (int)(a.K - next_n0 < kCols ? a.K - next_n0 : kCols);
+            next_stages = (int)((t.count + 63) / 64);
+            side_by_columns(sa, a.a + t.begin * a.K * 2, a.K * 2, t.count, next_n0);
+            side_by_columns(sb, a.b + t.begin * a.N * 2, a.N * 2, t.count, next_row0);
+        } else {
+            const int64_t m0 = (int64_t)t.m * MT;
+            next_row0 = t.begin + m0;
+            next_live_m = (int)(t.count - m0 < MT ? t.count - m0 : MT);
+            if constexpr (FORM == kDx) {
+                next_live_n = (int)(a.K - next_n0 < kCols ? a.K - next_n0 : kCols);
+                next_stages = (int)((a.N * 2 + kLine - 1) / kLine);
+                side_by_columns(sa, a.a + (int64_t)t.e * a.N * a.K * 2, a.K * 2, a.N, next_n0);
+                side_by_rows(sb, a.b + next_row0 * a.N * 2, a.N * 2, next_live_m, false);
+            } else {
+                const int64_t width = EPI == kPlain ? a.N : a.N / 2;
+                next_live_n = (int)(width - next_n0 < kCols ? width - next_n0 : kCols);
+                next_stages = (int)((a.K * eb + kLine - 1) / kLine);
+                const uint8_t *w = a.a + ((int64_t)t.e * a.N + next_n0) * a.K * eb;
+                side_by_rows(sa, w, a.K * eb, next_live_n, kUpByHalf);
+                sa.p2 = w + width * a.K * eb;
+                side_by_rows(sb, a.b + next_row0 * a.K * eb, a.K * eb, next_live_m, false);
+                if constexpr (FP8) {
+                    const int64_t G = a.K / 128, NB = (a.N + 127) / 128;
+                    const int64_t blk = next_n0 / 128;
+                    w_s = reinterpret_cast<const uint8_t *>(a.a_s + ((int64_t)t.e * NB + blk) * G);
+                    live_blocks = EPI != kPlain || NB - blk > 1 ? 2 : 1;
+                    live_rows = next_live_m;
+                    tok_s = a.b_s + 4 * (a.s_mat ? t.e * a.s_mat + m0 : next_row0 * a.s_row);
+                }
+            }
+        }
+        // one buffer's stages at least (empty ones read no memory): what is loaded is one tile ahead at most
+        if (next_stages < S::kBufs) next_stages = S::kBufs;
+        load_stages = next_stages;
+    }
+    // No tile to load: the operands are empty.
+    __device__ __forceinline__ void set_no_tile()
+    {
+        sa.bytes = sb.bytes = 0;
+        sa.depth = sb.depth = 0;
+        live_rows = live_blocks = 0;
+        load_stages = INT32_MAX;
+    }
+    __device__ __forceinline__ void take_tile()
+    {
+        row0 = next_row0;
+        n0 = next_n0;
+        begin = next_begin;
+        live_m = next_live_m;
+        live_n = next_live_n;
+        e = next_e;
+        stages = next_stages;
+    }
+
+    // ---- fragments ----
+    //
+    // A fragment is 16 rows (columns) of an operand and the whole stage of
+    // depth: lane l has row l % 16 and 16-byte chunks l / 16 and l / 16 + 4 of
+    // the stage's eight (by columns: the same depths).  The order of the depth
+    // is free as long as both operands share it: one v_mfma 16x16x128 takes
+    // all of it (fp8), two 16x16x32 a chunk each (bf16).  D has B's row l % 16
+    // and, in register i, A's row 4 (l / 16) + i.
+    template <bool COLS, int SIDE_ROWS>
+    __device__ __forceinline__ i32x8 fragment(uint32_t side, int f) const
+    {
+        u32x4 lo, hi;
+        if constexpr (COLS) {
+            static_assert(!COLS || SIDE_ROWS == 256, "512 bytes a depth row");
+            const int i = lane & 15, g = lane >> 4;
+            const uint32_t x = (uint32_t)((i >> 2) | (g & 1) << 2);
+            const uint8_t *p = lds + side + (uint32_t)(8 * g + (i >> 2)) * 512 + (((uint32_t)f ^ x) << 5) + (uint32_t)(i & 3) * 8;
+            auto tr = [&](int q) {
+                using lds_i16x4 = __attribute__((address_space(3))) i16x4;
+                return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + q * 512)));
+            };
+            const u32x2 a0 = tr(0), a1 = tr(4), b0 = tr(32), b1 = tr(36);
+            lo = u32x4{a0.x, a0.y, a1.x, a1.y};
+            hi = u32x4{b0.x, b0.y, b1.x, b1.y};
+        } else {
+            const uint32_t at = side + (uint32_t)(f * 16 + (lane & 15)) * kLine + (uint32_t)(((lane >> 4) ^ (lane >> 1 & 7)) << 4);
+            lo = *reinterpret_cast<const u32x4 *>(lds + at);
+            hi = *reinterpret_cast<const u32x4 *>(lds + (at ^ 64));
+        }
+        return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    }
+    __device__ __forceinline__ i32x8 a_fragment(int buf, int n) const
+    {
+        return fragment<S::kACols, kProductNT>((uint32_t)buf * S::kBuf, wn * NF + n);
+    }
+    __device__ __forceinline__ i32x8 b_fragment(int buf, int m) const
+    {
+        return fragment<S::kBCols, MT>((uint32_t)buf * S::kBuf + kProductNT * kLine, wm * MF + m);
+    }
+
+    // fp8: scale of the lane's row of fragment m in stage s of the batch in use
+    __device__ __forceinline__ float token_scale(int s, int m) const
+    {
+        const uint8_t *p = lds + S::kScales + (batch % kScaleRing) * S::kScaleBatch;
+        const int row = (wm * MF + m) * 16 + (lane & 15);
+        if (a.s_packed) {
+            const uint32_t c = (*reinterpret_cast<const uint32_t *>(p + row * 4) >> (8 * (s & 3))) & 255u;
+            return __uint_as_float(c == 0 ? 0x00400000u : c == 255 ? 0x7FC00000u : c << 23);
+        }
+        return *reinterpret_cast<const float *>(p + (a.s_row == 1 ? row * 4 + (s & 3) * (MT * 4) : row * 16 + (s & 3) * 4));
+    }
+    // of the wave's weight rows (SwiGLU: up = 0, 1 its gate, up rows)
+    __device__ __forceinline__ float weight_scale(int s, int up) const
+    {
+        const uint8_t *p = lds + S::kScales + (batch % kScaleRing) * S::kScaleBatch + MT * 16;
+        const int block = EPI == kPlain ? wn * NF * 16 / 128 : up;
+        return *reinterpret_cast<const float *>(p + block * 16 + (s & 3) * 4);
+    }
+
+    static __device__ __forceinline__ f32x4 mma(const i32x8 &x, const i32x8 &y, f32x4 c, int half)
+    {
+        const u32x4 u = half ? u32x4{(uint32_t)x[4], (uint32_t)x[5], (uint32_t)x[6], (uint32_t)x[7]}
+                             : u32x4{(uint32_t)x[0], (uint32_t)x[1], (uint32_t)x[2], (uint32_t)x[3]};
+        const u32x4 v = half ? u32x4{(uint32_t)y[4], (uint32_t)y[5], (uint32_t)y[6], (uint32_t)y[7]}
+                             : u32x4{(uint32_t)y[0], (uint32_t)y[1], (uint32_t)y[2], (uint32_t)y[3]};
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, u), __builtin_bit_cast(v8bf16, v), c, 0, 0, 0);
+    }
+
+    // Stage s of the tile, in LDS buffer buf, its first fragments in registers;
+    // leaves the next stage's there and loads a stage into buf.
+    template <bool BUSY, typename F>
+    __device__ __forceinline__ void run_stage(int buf, int s, F &&next)
+    {
+        const int nbuf = buf + 1 == S::kBufs ? 0 : buf + 1;
+        constexpr int kLeft = (S::kBufs - 2) * (S::kAUnits + S::kBUnits);
+        if constexpr (!BUSY) {
+            sync_stage<kLeft>();
+            load_next(buf, next);
+        } else {
+            float sc[MF], sc2[MF];
+            if constexpr (FP8) {
+                const bool real = (int64_t)s * kLine < a.K;  // a stage past the row's end has no scales
+                const float g = weight_scale(s, 0), u = EPI == kPlain ? 0.0f : weight_scale(s, 1);
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    const float t = token_scale(s, m);
+                    sc[m] = real ? t * g : 0.0f;
+                    sc2[m] = real && EPI != kPlain ? t * u : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                if (n == NF - D) {
+                    sync_stage<kLeft>();
+                    fa[(n + D) % R] = a_fragment(nbuf, (n + D) % NF);
+                    load_next(buf, next);
+                } else {
+                    fa[(n + D) % R] = a_fragment(n + D < NF ? buf : nbuf, (n + D) % NF);
+                }
+                if constexpr (FP8) {
+                    f32x4 p[MF];
+#pragma unroll
+                    for (int m = 0; m < MF; ++m) {
+                        p[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[n % R], fb[m], f32x4{}, 0, 0, 0, 0, 0, 0);
+                        if (n == NF - 1) fb[m] = b_fragment(nbuf, m);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MF; ++m) {
+                        const float f = EPI != kPlain && n >= NF / 2 ? sc2[m] : sc[m];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(p[m][i], f, acc[n][m][i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < MF; ++m) acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], 0);
+#pragma unroll
+                    for (int m = 0; m < MF; ++m) {
+                        acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], 1);
+                        if (n == NF - 1) fb[m] = b_fragment(nbuf, m);
+                    }
+                }
+            }
+        }
+    }
+
+    // A tile's products into acc; returns the buffer of the next tile's first
+    // stage.
+    template <bool BUSY, typename F>
+    __device__ __forceinline__ int run_tile(int buf, F &&next)
+    {
+        if constexpr (BUSY) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{};
+#pragma unroll
+            for (int j = 0; j < D; ++j) fa[j] = a_fragment(buf, j);
+#pragma unroll
+            for (int j = 0; j < MF; ++j) fb[j] = b_fragment(buf, j);
+        }
+        for (int s = 0; s < stages; ++s) {
+            run_stage<BUSY>(buf, s, next);
+            if (FP8 && ((s & 3) == 3 || s == stages - 1)) ++batch;
+            buf = buf + 1 == S::kBufs ? 0 : buf + 1;
+        }
+        return buf;
+    }
+
+    // ---- results ----
+
+    // NB blocks of 16 columns (from `col` of the row on) of the lane's row as
+    // bf16.  Four blocks: the lanes of a row trade (a 4 x 4 transpose over the
+    // four lanes of a row, then the halves of two blocks) so that each store
+    // writes 64 bytes in a run.
+    template <int NB>
+    __device__ __forceinline__ void store_blocks(const f32x4 (&v)[NB], uint16_t *row, int cols, bool live, bool vector) const
+    {
+        const int g = lane >> 4;
+        uint32_t lo[NB], hi[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            lo[j] = pack_bf16(v[j][0], v[j][1]);
+            hi[j] = pack_bf16(v[j][2], v[j][3]);
+        }
+        if (!vector) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 16 * j + 4 * g + i;
+                    if (live && c < cols) row[c] = (uint16_t)((i < 2 ? lo[j] : hi[j]) >> (16 * (i & 1)));
+                }
+        } else if constexpr (NB == 4) {
+            uint32_t *w[2] = {lo, hi};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                swap_halves(w[h][0], w[h][2]);
+                swap_halves(w[h][1], w[h][3]);
+                swap_rows16(w[h][0], w[h][1]);
+                swap_rows16(w[h][2], w[h][3]);
+            }
+            // block g: bytes 0-15 in lo, hi [0, 1], 16-31 in lo, hi [2, 3]
+            swap_halves(lo[0], lo[2]);
+            swap_halves(hi[0], hi[2]);
+            swap_halves(lo[1], lo[3]);
+            swap_halves(hi[1], hi[3]);
+            const int c = 16 * (g & 1) + 8 * (g >> 1);
+            if (live && c < cols) *reinterpret_cast<u32x4 *>(row + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+            if (live && c + 32 < cols) *reinterpret_cast<u32x4 *>(row + c + 32) = u32x4{lo[2], hi[2], lo[3], hi[3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int c = 16 * j + 4 * g;
+                if (live && c < cols) *reinterpret_cast<u32x2 *>(row + c) = u32x2{lo[j], hi[j]};
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store_tile() const
+    {
+        const int64_t ld = FORM == kFwd ? (EPI == kSwiglu ? a.N / 2 : a.N) : a.K;
+        const bool vector = ld % 8 == 0 && (EPI != kSwigluGrad || a.N / 2 % 8 == 0) && ((uintptr_t)a.out & 15) == 0;
+        const int64_t I = a.N / 2;
+        constexpr int H = EPI == kPlain ? NF : NF / 2;       // blocks of output columns
+        constexpr int NB = H < 4 ? H : 4;
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int t = (wm * MF + m) * 16 + (lane & 15);
+            const bool live = t < live_m;
+            uint16_t *row = a.out + (FORM == kDw ? (int64_t)e * a.N + row0 + t : row0 + t) * ld + n0;
+#pragma unroll
+            for (int q = 0; q < H / NB; ++q) {
+                const int c = (wn * H + q * NB) * 16;
+                f32x4 v[NB], w[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    if constexpr (EPI == kPlain) {
+                        v[j] = acc[q * NB + j][m];
+                    } else {
+                        const f32x4 gate = acc[q * NB + j][m], up = acc[H + q * NB + j][m];
+                        f32x4 d = {};
+                        if constexpr (EPI == kSwigluGrad) {
+                            const int at = c + 16 * j + 4 * (lane >> 4);
+                            const uint16_t *p = a.dh + (row0 + t) * I + n0 + at;
+                            if (live && ((I & 3) == 0 && ((uintptr_t)a.dh & 7) == 0)) {
+                                if (at < live_n) {
+                                    const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
+                                    d = f32x4{bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+                                }
+                            } else if (live) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (at + i < live_n) d[i] = __uint_as_float((uint32_t)p[i] << 16);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float s = 1.0f / (1.0f + __expf(-gate[i]));
+                            if constexpr (EPI == kSwiglu) {
+                                v[j][i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i];
+                            } else {
+                                v[j][i] = d[i] * up[i] * (s * (1.0f + gate[i] * (1.0f - s)));
+                                w[j][i] = d[i] * (gate[i] * s);
+                            }
+                        }
+                    }
+                }
+                store_blocks<NB>(v, row + c, live_n - c, live, vector);
+                if constexpr (EPI == kSwigluGrad) store_blocks<NB>(w, row + I + c, live_n - c, live, vector);
+                __builtin_amdgcn_sched_barrier(0);           // one group's temporaries at a time
+            }
+        }
+    }
+
+    // SwiGLU values in fp8: a tile's 128 columns are one group, so the waves
+    // of a row exchange their largest magnitudes.  Every wave comes here.
+    __device__ __forceinline__ void store_tile_fp8(bool busy)
+    {
+        constexpr int H = NF / 2;
+        float *amax = reinterpret_cast<float *>(lds + S::kAmax);
+        if (busy) {
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                uint32_t top = 0;                            // magnitudes as integers, NaNs left out
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float g = acc[j][m][i];
+                        const float h = g / (1.0f + __expf(-g)) * acc[H + j][m][i];
+                        acc[j][m][i] = h;
+                        const uint32_t u = __float_as_uint(h) & 0x7FFFFFFFu;
+                        top = u <= 0x7F800000u && u > top ? u : top;
+                    }
+                uint32_t o = top;
+                swap_halves(top, o);
+                top = top > o ? top : o;
+                o = top;
+                swap_rows16(top, o);
+                top = top > o ? top : o;
+                if (lane < 16) amax[wn * MT + (wm * MF + m) * 16 + lane] = __uint_as_float(top);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (!busy) return;
+        const int64_t I = a.N / 2;
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int t = (wm * MF + m) * 16 + (lane & 15);
+            float am = amax[t];
+#pragma unroll
+            for (int x = 1; x < S::WN; ++x) am = fmaxf(am, amax[x * MT + t]);
+            const Fp8Group q(am, (a.s_flags & CDL_FP8_SCALE_UE8M0) != 0);
+            const bool live = t < live_m;
+            const int64_t row = row0 + t;
+            uint32_t w[H];
+#pragma unroll
+            for (int j = 0; j < H; ++j) w[j] = q.code4(acc[j][m][0], acc[j][m][1], acc[j][m][2], acc[j][m][3]);
+            uint8_t *to = a.hq + row * I + n0 + wn * H * 16;
+            const int g = lane >> 4;
+            if constexpr (H == 4) {
+                swap_halves(w[0], w[2]);
+                swap_halves(w[1], w[3]);
+                swap_rows16(w[0], w[1]);
+                swap_rows16(w[2], w[3]);
+                if (live) *reinterpret_cast<u32x4 *>(to + 16 * g) = u32x4{w[0], w[1], w[2], w[3]};
+            } else {
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    if (live) *reinterpret_cast<uint32_t *>(to + 16 * j + 4 * g) = w[j];
+            }
+            if (live && lane < 16 && wn == 0) {
+                const int64_t grp = n0 / 128;
+                const int64_t r = a.h_mat ? e * a.h_mat + (row0 - (int64_t)e * a.cap + t) * a.h_row : row * a.h_row;
+                if (a.s_packed) {
+                    uint8_t *word = static_cast<uint8_t *>(a.hs) + (r + grp / 4 * a.h_group) * 4;
+                    word[grp % 4] = q.exponent();
+                    if (grp == I / 128 - 1)
+                        for (int64_t x = grp % 4 + 1; x < 4; ++x) word[x] = 0;
+                } else
+                    static_cast<float *>(a.hs)[r + grp * a.h_group] = q.scale;
+            }
+        }
+    }
+};
+
+// Tiles of the weights' gradient: the tile ids run over the experts, each with
+// tiles_m x tiles_n of them, whatever its count.
+__device__ __forceinline__ GroupedTile dw_tile(const ProductArgs &a, int tiles_m, int tiles_n, int64_t id)
+{
+    GroupedTile t;
+    const int64_t per = (int64_t)tiles_m * tiles_n;
+    t.e = __builtin_amdgcn_readfirstlane((int)(id / per));
+    const int local = (int)(id - t.e * per);
+    t.n = __builtin_amdgcn_readfirstlane(local / tiles_m);
+    t.m = __builtin_amdgcn_readfirstlane(local % tiles_m);
+    bool bad;
+    t.count = grouped_rows(a, t.e, &t.begin, &bad);
+    return t;
+}
+
+template <bool FP8, ProductForm FORM, ProductEpilogue EPI, int MT>
+__global__ __launch_bounds__(kProductThreads) void product_kernel(ProductArgs a, int tiles_m, int tiles_n)
+{
+    using Wg = ProductWg<FP8, FORM, EPI, MT>;
+    using S = ProductShape<FP8, FORM, MT>;
+    extern __shared__ u32x4 lds4[];
+    uint8_t *lds = reinterpret_cast<uint8_t *>(lds4);
+    int32_t *ends = reinterpret_cast<int32_t *>(lds + S::kLds);
+    // (kDw only checks the counts here: its tiles do not depend on them)
+    const int32_t counted = grouped_tile_table<MT>(a, FORM == kDw ? 1 : tiles_n, ends);
+    const int32_t total = FORM == kDw ? a.L * tiles_m * tiles_n : counted;
+    const int32_t per = (total + 7) / 8, step = (int32_t)(gridDim.x / 8);
+    const int32_t first = (int32_t)(blockIdx.x & 7) * per;
+    const int32_t last = first + per < total ? first + per : total;
+    int32_t id = first + (int32_t)(blockIdx.x >> 3);         // the tile being loaded
+    if (id >= last) return;
+    __syncthreads();
+    Wg w(a, lds);
+    auto tile = [&] { return FORM == kDw ? dw_tile(a, tiles_m, tiles_n, id) : grouped_tile(a, ends, tiles_n, id); };
+    auto next = [&] {
+        id += step;
+        if (id < last)
+            w.set_tile(tile());
+        else
+            w.set_no_tile();
+    };
+    w.set_tile(tile());
+    w.load_stage = 0;
+    for (int b = 0; b < S::kBufs; ++b) w.load_next(b, next);
+    sync_stage<(S::kBufs - 1) * (S::kAUnits + S::kBUnits)>();
+    int buf = 0;
+    for (int32_t at = id; at < last; at += step) {
+        w.take_tile();
+        const bool busy = w.wm * S::MF * 16 < w.live_m;      // the wave has a live row
+        buf = busy ? w.template run_tile<true>(buf, next) : w.template run_tile<false>(buf, next);
+        if constexpr (FP8 && EPI == kSwiglu)
+            w.store_tile_fp8(busy);
+        else if (busy)
+            w.store_tile();
+    }
+    // nothing may be on its way to this workgroup's LDS when it ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// A tile's operands are addressed with 32-bit offsets: 256 rows of at most
+// 2^22 bytes.
+inline int check_product(int64_t rows, int64_t K, int32_t L, int64_t N, const int32_t *counts, const int64_t *seg, int64_t cap)
+{
+    if (rows < 0 || K < 1 || N < 1 || L < 1 || L > CDL_MAX_LOCAL_EXPERTS) return CDL_ERR_BAD_SIZE;
+    if (!seg && (cap < 0 || rows != (int64_t)L * cap)) return CDL_ERR_BAD_SIZE;
+    if (K > CDL_MAX_PRODUCT_WIDTH || N > CDL_MAX_PRODUCT_WIDTH || rows > INT32_MAX) return CDL_ERR_TOO_LARGE;
+    if (!counts) return CDL_ERR_NULL_POINTER;
+    return CDL_OK;
+}
+
+template <bool FP8, ProductForm FORM, ProductEpilogue EPI, int MT>
+int launch_product_tiles(const ProductArgs &a, hipStream_t stream)
+{
+    using S = ProductShape<FP8, FORM, MT>;
+    constexpr int kCols = EPI == kPlain ? kProductNT : kProductNT / 2;
+    const int64_t width = FORM == kFwd ? (EPI == kPlain ? a.N : a.N / 2) : a.K;
+    const int64_t tiles_n = (width + kCols - 1) / kCols;
+    int64_t tiles, tiles_m = 0;
+    // tile numbers keep room for a workgroup's step past the last one
+    if (FORM == kDw) {
+        tiles_m = (a.N + MT - 1) / MT;
+        if (tiles_m * tiles_n > (INT32_MAX - kProductWgs) / a.L) return CDL_ERR_TOO_LARGE;
+        tiles = a.L * tiles_m * tiles_n;
+    } else {
+        const int64_t most = a.seg ? a.rows : a.cap;
+        if ((most + MT - 1) / MT * tiles_n > (INT32_MAX - kProductWgs) / a.L) return CDL_ERR_TOO_LARGE;
+        tiles = (a.seg ? a.rows / MT + a.L : (int64_t)a.L * ((a.cap + MT - 1) / MT)) * tiles_n;
+    }
+    const int64_t filled = (tiles + 7) / 8 * 8, wgs = filled ? filled : 8;       // (none: the counts' check)
+    product_kernel<FP8, FORM, EPI, MT><<<dim3((unsigned)(wgs < kProductWgs ? wgs : kProductWgs)), dim3(kProductThreads),
+                                         S::kLds + (size_t)a.L * sizeof(int32_t), stream>>>(a, (int)tiles_m, (int)tiles_n);
+    return launch_status();
+}
+
+template <bool FP8, ProductForm FORM, ProductEpilogue EPI>
+int launch_product(const ProductArgs &a, hipStream_t stream)
+{
+    if constexpr (FORM == kDw) {
+        return launch_product_tiles<FP8, FORM, EPI, 256>(a, stream);
+    } else {
+        // (an empty buffer: only the check of the counts is left)
+        if (a.rows == 0 && !a.status) return CDL_OK;
+        const int64_t small_tiles = (a.rows / 64 + a.L / 2) * ((a.N + kProductNT - 1) / kProductNT);
+        const bool large = a.seg ? a.rows / a.L >= 64 && small_tiles > kProductWgs : a.cap > 256;
+        return large ? launch_product_tiles<FP8, FORM, EPI, 256>(a, stream) : launch_product_tiles<FP8, FORM, EPI, 64>(a, stream);
+    }
+}
+
+inline ProductArgs product_args(const void *a, const void *b, int64_t rows, int64_t K, int32_t L, int64_t N,
+                                const int32_t *counts, const int64_t *seg, int64_t cap, uint16_t *out, int32_t *status)
+{
+    ProductArgs p = {};
+    p.a = static_cast<const uint8_t *>(a);
+    p.b = static_cast<const uint8_t *>(b);
+    p.rows = rows;
+    p.K = K;
+    p.L = L;
+    p.N = N;
+    p.counts = counts;
+    p.seg = seg;
+    p.cap = cap;
+    p.out = out;
+    p.status = status;
+    return p;
+}
+
+// The words of a scale buffer of `rows` rows and G groups (padded buffers:
+// cap rows a matrix where it is column-major).
+struct ScaleWords {
+    int64_t row, batch, group, mat;
+    ScaleWords(int32_t flags, int64_t rows, int64_t cap, bool padded, int64_t G)
+    {
+        const bool packed = (flags & CDL_FP8_SCALE_PACKED) != 0;
+        const int64_t words = packed ? (G + 3) / 4 : G;
+        group = mat = 0;
+        if (flags & CDL_FP8_SCALE_COLMAJOR) {
+            const int64_t ld = ((padded ? cap : rows) + 3) / 4 * 4;
+            row = 1;
+            batch = packed ? ld : 4 * ld;
+            group = packed ? 0 : ld;
+            mat = padded ? words * ld : 0;
+        } else {
+            row = words;
+            batch = packed ? 1 : 4;
+        }
+    }
+};
+
+inline int check_fp8_product(const uint8_t *q, const void *s, const uint8_t *wq, const float *ws, int64_t rows, int64_t K,
+                             int32_t flags)
+{
+    if (!wq || !ws || (rows > 0 && (!q || !s))) return CDL_ERR_NULL_POINTER;
+    if (K % CDL_FP8_GROUP != 0 || !valid_scale_flags(flags)) return CDL_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(wq, 16) || !aligned(s, 4) || !aligned(ws, 4)) return CDL_ERR_UNSUPPORTED;
+    return CDL_OK;
+}
+
+inline void set_fp8(ProductArgs &p, const void *s, const float *ws, int32_t flags)
+{
+    const ScaleWords w(flags, p.rows, p.cap, p.seg == nullptr, p.K / CDL_FP8_GROUP);
+    p.b_s = static_cast<const uint8_t *>(s);
+    p.a_s = ws;
+    p.s_row = w.row;
+    p.s_batch = w.batch;
+    p.s_group = w.group;
+    p.s_mat = w.mat;
+    p.s_packed = (flags & CDL_FP8_SCALE_PACKED) != 0;
+    p.s_flags = flags;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cdl_grouped_bf16(const uint16_t *x, int64_t rows, int64_t K, const uint16_t *w, int32_t L, int64_t N,
+                     const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *out, int32_t *status,
+                     void *stream)
+{
+    int rc = check_product(rows, K, L, N, counts, seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (!w || (rows > 0 && (!x || !out))) return CDL_ERR_NULL_POINTER;
+    if (K % 8 != 0 || !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 2)) return CDL_ERR_UNSUPPORTED;
+    return launch_product<false, kFwd, kPlain>(product_args(w, x, rows, K, L, N, counts, seg_indptr, cap, out, status),
+                                               (hipStream_t)stream);
+}
+
+int cdl_grouped_swiglu_bf16(const uint16_t *x, int64_t rows, int64_t K, const uint16_t *w, int32_t L, int64_t I,
+                            const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *out, int32_t *status,
+                            void *stream)
+{
+    int rc = check_product(rows, K, L, I < 1 ? I : 2 * (I < CDL_MAX_PRODUCT_WIDTH ? I : CDL_MAX_PRODUCT_WIDTH), counts,
+                           seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (!w || (rows > 0 && (!x || !out))) return CDL_ERR_NULL_POINTER;
+    if (K % 8 != 0 || !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 2)) return CDL_ERR_UNSUPPORTED;
+    return launch_product<false, kFwd, kSwiglu>(product_args(w, x, rows, K, L, 2 * I, counts, seg_indptr, cap, out, status),
+                                                (hipStream_t)stream);
+}
+
+int cdl_grouped_swiglu_bf16_grad(const uint16_t *x, int64_t rows, int64_t K, const uint16_t *w, int32_t L, int64_t I,
+                                 const uint16_t *dh, const int32_t *counts, const int64_t *seg_indptr, int64_t cap,
+                                 uint16_t *out, int32_t *status, void *stream)
+{
+    int rc = check_product(rows, K, L, I < 1 ? I : 2 * (I < CDL_MAX_PRODUCT_WIDTH ? I : CDL_MAX_PRODUCT_WIDTH), counts,
+                           seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (!w || (rows > 0 && (!x || !dh || !out))) return CDL_ERR_NULL_POINTER;
+    if (K % 8 != 0 || !aligned(x, 16) || !aligned(w, 16) || !aligned(dh, 2) || !aligned(out, 2)) return CDL_ERR_UNSUPPORTED;
+    ProductArgs a = product_args(w, x, rows, K, L, 2 * I, counts, seg_indptr, cap, out, status);
+    a.dh = dh;
+    return launch_product<false, kFwd, kSwigluGrad>(a, (hipStream_t)stream);
+}
+
+int cdl_grouped_bf16_dx(const uint16_t *dy, int64_t rows, int64_t N, const uint16_t *w, int32_t L, int64_t K,
+                        const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *dx, int32_t *status,
+                        void *stream)
+{
+    int rc = check_product(rows, K, L, N, counts, seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (!w || (rows > 0 && (!dy || !dx))) return CDL_ERR_NULL_POINTER;
+    if (K % 8 != 0 || N % 8 != 0 || !aligned(dy, 16) || !aligned(w, 16) || !aligned(dx, 16)) return CDL_ERR_UNSUPPORTED;
+    return launch_product<false, kDx, kPlain>(product_args(w, dy, rows, K, L, N, counts, seg_indptr, cap, dx, status),
+                                              (hipStream_t)stream);
+}
+
+int cdl_grouped_bf16_dw(const uint16_t *dy, const uint16_t *x, int64_t rows, int64_t N, int64_t K, int32_t L,
+                        const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *dw, int32_t *status,
+                        void *stream)
+{
+    int rc = check_product(rows, K, L, N, counts, seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (!dw || (rows > 0 && (!dy || !x))) return CDL_ERR_NULL_POINTER;
+    if (K % 8 != 0 || N % 8 != 0 || !aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16)) return CDL_ERR_UNSUPPORTED;
+    return launch_product<false, kDw, kPlain>(product_args(x, dy, rows, K, L, N, counts, seg_indptr, cap, dw, status),
+                                              (hipStream_t)stream);
+}
+
+int cdl_grouped_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, int64_t rows, int64_t K, const uint8_t *w_q,
+                    const float *w_scales, int32_t L, int64_t N, const int32_t *counts, const int64_t *seg_indptr,
+                    int64_t cap, uint16_t *out, int32_t *status, void *stream)
+{
+    int rc = check_product(rows, K, L, N, counts, seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (rows > 0 && !out) return CDL_ERR_NULL_POINTER;
+    rc = check_fp8_product(q, scales, w_q, w_scales, rows, K, scale_flags);
+    if (rc != CDL_OK) return rc;
+    if (!aligned(out, 2)) return CDL_ERR_UNSUPPORTED;
+    ProductArgs a = product_args(w_q, q, rows, K, L, N, counts, seg_indptr, cap, out, status);
+    set_fp8(a, scales, w_scales, scale_flags);
+    return launch_product<true, kFwd, kPlain>(a, (hipStream_t)stream);
+}
+
+int cdl_grouped_swiglu_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, int64_t rows, int64_t K,
+                           const uint8_t *w_q, const float *w_scales, int32_t L, int64_t I, const int32_t *counts,
+                           const int64_t *seg_indptr, int64_t cap, uint8_t *out_q, void *out_scales, int32_t *status,
+                           void *stream)
+{
+    int rc = check_product(rows, K, L, I < 1 ? I : 2 * (I < CDL_MAX_PRODUCT_WIDTH ? I : CDL_MAX_PRODUCT_WIDTH), counts,
+                           seg_indptr, cap);
+    if (rc != CDL_OK) return rc;
+    if (rows > 0 && (!out_q || !out_scales)) return CDL_ERR_NULL_POINTER;
+    rc = check_fp8_product(q, scales, w_q, w_scales, rows, K, scale_flags);
+    if (rc != CDL_OK) return rc;
+    if (I % CDL_FP8_GROUP != 0 || !aligned(out_q, 16) || !aligned(out_scales, 4)) return CDL_ERR_UNSUPPORTED;
+    ProductArgs a = product_args(w_q, q, rows, K, L, 2 * I, counts, seg_indptr, cap, nullptr, status);
+    set_fp8(a, scales, w_scales, scale_flags);
+    const ScaleWords h(scale_flags, rows, cap, seg_indptr == nullptr, I / CDL_FP8_GROUP);
+    a.hq = out_q;
+    a.hs = out_scales;
+    a.h_row = h.row;
+    a.h_group = a.s_packed ? h.batch : h.group ? h.group : 1;
+    a.h_mat = h.mat;
+    return launch_product<true, kFwd, kSwiglu>(a, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -80,6 +80,7 @@ extern "C" {
 #define CDL_FP8_GROUP 128
 #define CDL_MXFP4_GROUP 32
 #define CDL_MOE_LAYER_MAX_TOKENS 128
+#define CDL_MAX_PRODUCT_WIDTH (1 << 21)  /* K and N (SwiGLU: 2 I) of the bf16 and fp8 products */
 
 /* fp8 scale formats (bit flags) -- see cdl_dispatch_fp8_ex */
 #define CDL_FP8_SCALE_UE8M0 1       /* power-of-two scales */
@@ -641,6 +642,176 @@ int cdl_moe_layer_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
                         int32_t L, int64_t I, const uint8_t *w13_q, const uint8_t *w13_scales,
                         const uint8_t *w2_q, const uint8_t *w2_scales, uint16_t *out, void *ws,
                         size_t ws_bytes, void *stream);
+
+/*
+ * Products grouped by expert, in bf16 and in fp8.  Rows, counts, seg_indptr,
+ * cap and status are those of cdl_grouped_mxfp4: expert e owns counts[e] rows
+ * from seg_indptr[e] (segments may be padded), or, with seg_indptr NULL, from
+ * e * cap of a padded buffer of L * cap rows; a count that does not fit the
+ * buffer is cut to what does and reported; rows of no expert are neither read
+ * nor written.  Sums are taken in fp32 and rounded once.  K and N at most
+ * CDL_MAX_PRODUCT_WIDTH; CDL_ERR_TOO_LARGE also where L times the output tiles
+ * of one expert that owns the whole buffer (64 or 256 rows, 256 columns)
+ * exceeds 2^31 - 257.
+ */
+
+/*
+ * cdl_grouped_bf16 -- each dispatched row times its expert's weights:
+ * out[r, n] = bf16_rne(sum_k x[r, k] * w[e, n, k]).
+ *   x    in  [rows, K] bf16, 16-byte aligned, K % 8 == 0
+ *   w    in  [L, N, K] bf16, 16-byte aligned
+ *   out  out [rows, N] bf16, any N
+ */
+int cdl_grouped_bf16(const uint16_t *x, int64_t rows, int64_t K, const uint16_t *w, int32_t L, int64_t N,
+                     const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *out,
+                     int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_swiglu_bf16 -- the gate/up product with SwiGLU in its epilogue:
+ * with w [L, 2 I, K] the I gate rows followed by the I up rows of every expert
+ * and g, u the two products in fp32, out[r, i] = bf16_rne(g / (1 + exp(-g)) * u)
+ * [rows, I].
+ */
+int cdl_grouped_swiglu_bf16(const uint16_t *x, int64_t rows, int64_t K, const uint16_t *w, int32_t L, int64_t I,
+                            const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *out,
+                            int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_swiglu_bf16_grad -- the gradient of its gate and up values, which
+ * it computes again from x and w (none are kept): with s = 1 / (1 + exp(-g)),
+ *   out[r, i]     = bf16_rne(dh[r, i] * u * s * (1 + g * (1 - s)))
+ *   out[r, I + i] = bf16_rne(dh[r, i] * g * s)
+ * [rows, 2 I], the dy of cdl_grouped_bf16_dx and cdl_grouped_bf16_dw (bf16
+ * because those products take bf16).  dh [rows, I] bf16.
+ */
+int cdl_grouped_swiglu_bf16_grad(const uint16_t *x, int64_t rows, int64_t K, const uint16_t *w, int32_t L,
+                                 int64_t I, const uint16_t *dh, const int32_t *counts, const int64_t *seg_indptr,
+                                 int64_t cap, uint16_t *out, int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_bf16_dx -- the gradient of cdl_grouped_bf16's rows:
+ * dx[r, k] = bf16_rne(sum_n dy[r, n] * w[e, n, k]).  dy [rows, N], w [L, N, K]
+ * as it lies, dx [rows, K]; all 16-byte aligned, K % 8 == 0 and N % 8 == 0.
+ */
+int cdl_grouped_bf16_dx(const uint16_t *dy, int64_t rows, int64_t N, const uint16_t *w, int32_t L, int64_t K,
+                        const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *dx,
+                        int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_bf16_dw -- the gradient of its weights:
+ * dw[e, n, k] = bf16_rne(sum over e's rows of dy[r, n] * x[r, k]), [L, N, K],
+ * every element written (an expert of no rows gets zeros), in a fixed order:
+ * the result is deterministic.  Alignment as for cdl_grouped_bf16_dx.
+ */
+int cdl_grouped_bf16_dw(const uint16_t *dy, const uint16_t *x, int64_t rows, int64_t N, int64_t K, int32_t L,
+                        const int32_t *counts, const int64_t *seg_indptr, int64_t cap, uint16_t *dw,
+                        int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_fp8 -- each dispatched fp8 row times its expert's fp8 weights:
+ *   out[r, n] = bf16_rne(sum over groups g of (s[r, g] * w_scales[e, n / 128, g])
+ *                        * sum over k of g of q[r, k] * w_q[e, n, k])
+ *   q, scales  in  [rows, K] E4M3FN bytes and their scales in any scale_flags
+ *                  format of cdl_dispatch_fp8_ex, for `rows` rows (padded
+ *                  buffers: every expert's cap rows one column-major matrix):
+ *                  what the fp8 dispatches write
+ *   w_q        in  [L, N, K] E4M3FN bytes
+ *   w_scales   in  [L, ceil(N / 128), K / 128] fp32, one for each block of
+ *                  128 x 128 weights (cdl_quant_fp8_blocks)
+ *   out        out [rows, N] bf16, any N
+ * K % 128 == 0; q and w_q 16-byte, scales 4-byte aligned.  The matrix
+ * instruction drops what lies below 2^-13 of the largest product among 8
+ * neighbouring ones before it adds them; the sums of those, and all others,
+ * are fp32.
+ */
+int cdl_grouped_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, int64_t rows, int64_t K,
+                    const uint8_t *w_q, const float *w_scales, int32_t L, int64_t N, const int32_t *counts,
+                    const int64_t *seg_indptr, int64_t cap, uint16_t *out, int32_t *status, void *stream);
+
+/*
+ * cdl_grouped_swiglu_fp8 -- the gate/up product with SwiGLU and quantisation in
+ * its epilogue: w_q [L, 2 I, K], the I gate rows and then the I up rows of
+ * every expert; h = g / (1 + exp(-g)) * u in fp32, quantised in groups of 128
+ * as by the fp8 dispatch into out_q [rows, I] (16-byte aligned) and out_scales
+ * in the scale_flags format of the input: the operand of the down product.
+ * I % 128 == 0; the rest as cdl_grouped_fp8.
+ */
+int cdl_grouped_swiglu_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, int64_t rows, int64_t K,
+                           const uint8_t *w_q, const float *w_scales, int32_t L, int64_t I, const int32_t *counts,
+                           const int64_t *seg_indptr, int64_t cap, uint8_t *out_q, void *out_scales,
+                           int32_t *status, void *stream);
+
+/*
+ * cdl_quant_fp8_blocks -- bf16 weights [mats, N, K] to E4M3FN bytes with one
+ * fp32 scale for each block of 128 x 128 (the last block of rows may be
+ * shorter), once at load: s = amax / 448 and the codes as cdl_dispatch_fp8's.
+ *   w       in  [mats, N, K] bf16, 16-byte aligned, K % 128 == 0
+ *   q       out [mats, N, K] bytes, 8-byte aligned
+ *   scales  out [mats, ceil(N / 128), K / 128] fp32
+ */
+int cdl_quant_fp8_blocks(const uint16_t *w, int64_t mats, int64_t N, int64_t K, uint8_t *q, float *scales,
+                         void *stream);
+
+/*
+ * cdl_dequant_fp8 -- fp8 rows and their scales in any scale_flags format back
+ * to bf16: out = bf16_rne(code * scale).  Every rows_per_mat rows form one
+ * column-major matrix (rows in normal mode, cap in the padded buffer).  q and
+ * out 16-byte aligned, H % 128 == 0.
+ */
+int cdl_dequant_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, int64_t rows, int64_t H,
+                    int64_t rows_per_mat, uint16_t *out, void *stream);
+
+/*
+ * cdl_rms_norm -- the norm before a layer, with the residual's addition:
+ *   h[t] = residual ? bf16_rne(x[t] + residual[t]) : x[t]
+ *   out[t, c] = bf16_rne(h[t, c] / sqrt(mean(h[t]^2) + eps) * weight[c])
+ * in fp32.  h is rounded before it is normed: the norm is that of the rows the
+ * residual path keeps, as by two separate calls.
+ *   x, residual   in  [T, H] bf16 (residual may be NULL)
+ *   weight        in  [H] bf16
+ *   out           out [T, H] bf16
+ *   residual_out  out [T, H] bf16: h (required with residual, else ignored)
+ * out and residual_out may each be x or residual itself; no other overlap.
+ * Any H from 1 to CDL_MAX_HIDDEN (a multiple of 8 with 16-byte aligned arrays
+ * takes the vector path); eps >= 0.
+ */
+int cdl_rms_norm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps, int64_t T,
+                 int64_t H, uint16_t *out, uint16_t *residual_out, void *stream);
+
+/*
+ * cdl_rms_norm_fp8 -- cdl_rms_norm whose fp32 result is quantised in groups of
+ * 128 as cdl_dispatch_fp8_ex quantises rows (same scales, formats and
+ * non-finite values): the rows of an fp8 product that no dispatch precedes.
+ *   out_q       out [T, H] E4M3FN bytes, 8-byte aligned
+ *   out_scales  out in the scale_flags format for T rows
+ *   out         out [T, H] bf16, or NULL: the unquantised rows as well
+ * H % 128 == 0; the bf16 arrays 16-byte aligned.
+ */
+int cdl_rms_norm_fp8(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps, int64_t T,
+                     int64_t H, uint8_t *out_q, void *out_scales, int32_t scale_flags, uint16_t *out,
+                     uint16_t *residual_out, void *stream);
+
+/*
+ * cdl_rms_norm_grad_workspace_size -- device workspace bytes of
+ * cdl_rms_norm_grad (partial sums of dweight); 0 for rejected sizes.  It does
+ * not shrink as T grows.
+ */
+size_t cdl_rms_norm_grad_workspace_size(int64_t T, int64_t H);
+
+/*
+ * cdl_rms_norm_grad -- the gradient of cdl_rms_norm: with h the rows it normed,
+ * r = 1 / sqrt(mean(h^2) + eps), n = h r and d = dy weight,
+ *   dx[t]      = bf16_rne(r (d - n mean(d n)) + dresidual[t])
+ *   dweight[c] = sum over t of dy[t, c] n[t, c]          (fp32)
+ * dx is the gradient of h, so of x and of residual alike; dresidual [T, H] bf16,
+ * the gradient that reaches h past the norm, may be NULL.  dx may be dy, h or
+ * dresidual itself.  T == 0 gives zeros.  Sums are taken in a fixed order: the
+ * result is deterministic.  ws: cdl_rms_norm_grad_workspace_size bytes, 8-byte
+ * aligned, no initialisation needed; calls that overlap need their own.
+ */
+int cdl_rms_norm_grad(const uint16_t *dy, const uint16_t *h, const uint16_t *weight, const uint16_t *dresidual,
+                      float eps, int64_t T, int64_t H, uint16_t *dx, float *dweight, void *ws, size_t ws_bytes,
+                      void *stream);
 
 /*
  * cdl_ll_expected_m -- host-side hint for the masked grouped GEMM after a
