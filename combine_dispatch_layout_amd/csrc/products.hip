@@ -162,7 +162,7 @@ struct ProductShape {
     static constexpr bool kACols = FORM != kFwd, kBCols = FORM == kDw;
     static constexpr int kBufs = MT == 256 ? 2 : 3;
     static constexpr int kBuf = (kProductNT + MT) * kLine;
-    static constexpr int kAUnits = 4, kBUnits = MT / 64; // loads per wave and stage
+    static constexpr int kAUnits = 4, kUnits = 4 + MT / 64;   // loads per wave and stage (of A first)
     static constexpr int kScaleBatch = MT * 16 + 1024;   // token scales, then the weights'
     static constexpr int kScales = kBufs * kBuf;
     static constexpr int kAmax = kScales + (FP8 ? kScaleRing * kScaleBatch : 0);
@@ -184,13 +184,15 @@ struct ProductWg {
     using S = ProductShape<FP8, FORM, MT>;
     static constexpr int kCols = EPI == kPlain ? kProductNT : kProductNT / 2;     // output columns of a tile
     static constexpr int NF = S::NF, MF = S::MF;
-    static constexpr int R = 2, D = R - 1;                     // fragments of A in registers, read ahead
+    static constexpr int R = FP8 ? 2 : 4, D = R - 1;           // fragments of A in registers, read ahead
+    static_assert(NF % R == 0, "a fragment's registers do not depend on the stage");
     static constexpr bool kUpByUnit = EPI != kPlain && S::WN == 2, kUpByHalf = EPI != kPlain && S::WN == 4;
 
     const ProductArgs a;
     uint8_t *const lds;
     const int tid, lane, wave, wn, wm;
     const uint32_t lds0;                     // LDS address of the buffers
+    const uint32_t a_lane, b_lane;           // a lane's place in the wave's first fragments
     // operands being loaded
     ProductSide sa, sb;
     int load_stage, load_stages;
@@ -205,10 +207,13 @@ struct ProductWg {
 
     f32x4 acc[NF][MF];
     i32x8 fa[R], fb[MF];
+    f32x4 part[MF];                          // fp8: the sums of a stage of the A fragment before, and their scales
+    float part_s[MF];
 
     __device__ __forceinline__ ProductWg(const ProductArgs &args, uint8_t *l)
         : a(args), lds(l), tid(threadIdx.x), lane(tid & (kWave - 1)), wave(wave_id()), wn(wave % S::WN), wm(wave / S::WN),
-          lds0(lds_address(l)), load_batch(0), batch(0)
+          lds0(lds_address(l)), a_lane(fragment_lane<S::kACols>(wn * S::NF)), b_lane(fragment_lane<S::kBCols>(wm * S::MF)),
+          load_batch(0), batch(0)
     {
     }
 
@@ -244,34 +249,39 @@ struct ProductWg {
         s.off = at < s.ld ? (uint32_t)(2 * wave + (lane >> 5)) * s.ld + at : kFar;
     }
 
-    // Stage s of a side to LDS address `to`.
-    template <int UNITS, bool COLS, bool IS_A>
-    __device__ __forceinline__ void load_side(const ProductSide &s, int stage, uint32_t to) const
+    // The loads of one stage, unit by unit.
+    struct Units {
+        u32x4 ra, ra2, rb;
+        uint32_t a_off, b_off, to;
+    };
+    template <bool COLS>
+    __device__ __forceinline__ u32x4 side_rsrc(const ProductSide &s, const uint8_t *p, int stage) const
     {
         if constexpr (COLS) {
-            const int64_t d0 = (int64_t)stage * 64;
-            const int64_t left = s.depth - d0;
-            const u32x4 r = scalar_rsrc(s.p + d0 * s.ld, (uint32_t)(left <= 0 ? 0 : left < 64 ? left : 64) * s.ld);
-            uint32_t off = s.off;
-#pragma unroll
-            for (int j = 0; j < UNITS; ++j, off += 16 * s.ld) dma16(r, off, to + wave * 1024 + j * 8192);
+            const int64_t d0 = (int64_t)stage * 64, left = s.depth - d0;
+            return scalar_rsrc(p + d0 * s.ld, (uint32_t)(left <= 0 ? 0 : left < 64 ? left : 64) * s.ld);
+        } else {
+            return scalar_rsrc(p, s.bytes);
+        }
+    }
+    template <bool COLS>
+    __device__ __forceinline__ uint32_t side_off(const ProductSide &s, int stage) const
+    {
+        if constexpr (COLS) {
+            return s.off;
         } else {
             const uint32_t k = (uint32_t)stage * kLine;
-            uint32_t off = k + row_chunk() * 16 < s.ld ? s.off + k : kFar;
-            const u32x4 r = scalar_rsrc(s.p, s.bytes);
-            if constexpr (IS_A && kUpByUnit) {
-                const u32x4 r2 = scalar_rsrc(s.p2, s.bytes);
-#pragma unroll
-                for (int j = 0; j < UNITS; ++j) {
-                    dma16(j & 1 ? r2 : r, off, to + wave * 1024 + j * 8192);
-                    if (j & 1) off += 64 * s.ld;
-                }
-            } else {
-                const u32x4 rr = IS_A && kUpByHalf && wave >= 4 ? scalar_rsrc(s.p2, s.bytes) : r;
-#pragma unroll
-                for (int j = 0; j < UNITS; ++j, off += (IS_A && kUpByHalf ? 32 : 64) * s.ld)
-                    dma16(rr, off, to + wave * 1024 + j * 8192);
-            }
+            return k + row_chunk() * 16 < s.ld ? s.off + k : kFar;
+        }
+    }
+    __device__ __forceinline__ void load_unit(Units &u, int j) const
+    {
+        if (j < S::kAUnits) {
+            dma16(kUpByUnit && (j & 1) ? u.ra2 : u.ra, u.a_off, u.to + j * 8192);
+            if (!kUpByUnit || (j & 1)) u.a_off += (S::kACols ? 16 : kUpByHalf ? 32 : 64) * sa.ld;
+        } else {
+            dma16(u.rb, u.b_off, u.to + j * 8192);
+            u.b_off += (S::kBCols ? 16 : 64) * sb.ld;
         }
     }
 
@@ -309,19 +319,32 @@ struct ProductWg {
         ++load_batch;
     }
 
-    // The next stage in order to buffer `buf`; next() moves to the next tile.
+    // Begins the loads of the next stage in order to buffer `buf`; next() moves
+    // to the next tile.
     template <typename F>
-    __device__ __forceinline__ void load_next(int buf, F &&next)
+    __device__ __forceinline__ Units begin_load(int buf, F &&next)
     {
         if (load_stage == load_stages) {
             next();
             load_stage = 0;
         }
         if (FP8 && (load_stage & 3) == 0) load_scales(load_stage >> 2);
-        const uint32_t to = lds0 + (uint32_t)buf * S::kBuf;
-        load_side<S::kAUnits, S::kACols, true>(sa, load_stage, to);
-        load_side<S::kBUnits, S::kBCols, false>(sb, load_stage, to + kProductNT * kLine);
+        Units u;
+        u.ra = side_rsrc<S::kACols>(sa, kUpByHalf && wave >= 4 ? sa.p2 : sa.p, load_stage);
+        if (kUpByUnit) u.ra2 = side_rsrc<S::kACols>(sa, sa.p2, load_stage);
+        u.rb = side_rsrc<S::kBCols>(sb, sb.p, load_stage);
+        u.a_off = side_off<S::kACols>(sa, load_stage);
+        u.b_off = side_off<S::kBCols>(sb, load_stage);
+        u.to = lds0 + (uint32_t)buf * S::kBuf + (uint32_t)wave * 1024;
         ++load_stage;
+        return u;
+    }
+    template <typename F>
+    __device__ __forceinline__ void load_next(int buf, F &&next)
+    {
+        Units u = begin_load(buf, next);
+#pragma unroll
+        for (int j = 0; j < S::kUnits; ++j) load_unit(u, j);
     }
 
     // Sets what is loaded to tile `id`.
@@ -396,48 +419,60 @@ struct ProductWg {
     // is free as long as both operands share it: one v_mfma 16x16x128 takes
     // all of it (fp8), two 16x16x32 a chunk each (bf16).  D has B's row l % 16
     // and, in register i, A's row 4 (l / 16) + i.
-    template <bool COLS, int SIDE_ROWS>
-    __device__ __forceinline__ i32x8 fragment(uint32_t side, int f) const
+    template <bool COLS>
+    __device__ __forceinline__ uint32_t fragment_lane(int first) const       // first: the wave's first fragment
+    {
+        const int i = lane & 15, g = lane >> 4;
+        if constexpr (COLS) {
+            const uint32_t x = (uint32_t)((i >> 2) | (g & 1) << 2);
+            return (uint32_t)(8 * g + (i >> 2)) * 512 + (((uint32_t)first ^ x) << 5) + (uint32_t)(i & 3) * 8;
+        } else {
+            return (uint32_t)(first * 16 + i) * kLine + (uint32_t)((g ^ (i >> 1)) << 4);
+        }
+    }
+    // fragment f of the wave's, from the buffer that begins at `at`; by rows
+    // the two chunks are 64 bytes apart, swizzled
+    template <bool COLS>
+    __device__ __forceinline__ i32x8 fragment(uint32_t at, uint32_t of_lane, int f) const
     {
         u32x4 lo, hi;
         if constexpr (COLS) {
-            static_assert(!COLS || SIDE_ROWS == 256, "512 bytes a depth row");
-            const int i = lane & 15, g = lane >> 4;
-            const uint32_t x = (uint32_t)((i >> 2) | (g & 1) << 2);
-            const uint8_t *p = lds + side + (uint32_t)(8 * g + (i >> 2)) * 512 + (((uint32_t)f ^ x) << 5) + (uint32_t)(i & 3) * 8;
+            const uint32_t p = at + (of_lane ^ (uint32_t)(f << 5));
             auto tr = [&](int q) {
                 using lds_i16x4 = __attribute__((address_space(3))) i16x4;
-                return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + q * 512)));
+                return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(p + q * 512)));
             };
             const u32x2 a0 = tr(0), a1 = tr(4), b0 = tr(32), b1 = tr(36);
             lo = u32x4{a0.x, a0.y, a1.x, a1.y};
             hi = u32x4{b0.x, b0.y, b1.x, b1.y};
         } else {
-            const uint32_t at = side + (uint32_t)(f * 16 + (lane & 15)) * kLine + (uint32_t)(((lane >> 4) ^ (lane >> 1 & 7)) << 4);
-            lo = *reinterpret_cast<const u32x4 *>(lds + at);
-            hi = *reinterpret_cast<const u32x4 *>(lds + (at ^ 64));
+            using lds_u32x4 = __attribute__((address_space(3))) const u32x4;
+            lo = *(lds_u32x4 *)(uintptr_t)(at + of_lane + f * (16 * kLine));
+            hi = *(lds_u32x4 *)(uintptr_t)(at + (of_lane ^ 64) + f * (16 * kLine));
         }
         return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
     }
     __device__ __forceinline__ i32x8 a_fragment(int buf, int n) const
     {
-        return fragment<S::kACols, kProductNT>((uint32_t)buf * S::kBuf, wn * NF + n);
+        return fragment<S::kACols>(lds0 + (uint32_t)buf * S::kBuf, a_lane, n);
     }
     __device__ __forceinline__ i32x8 b_fragment(int buf, int m) const
     {
-        return fragment<S::kBCols, MT>((uint32_t)buf * S::kBuf + kProductNT * kLine, wm * MF + m);
+        return fragment<S::kBCols>(lds0 + (uint32_t)buf * S::kBuf + kProductNT * kLine, b_lane, m);
     }
 
     // fp8: scale of the lane's row of fragment m in stage s of the batch in use
     __device__ __forceinline__ float token_scale(int s, int m) const
     {
-        const uint8_t *p = lds + S::kScales + (batch % kScaleRing) * S::kScaleBatch;
-        const int row = (wm * MF + m) * 16 + (lane & 15);
-        if (a.s_packed) {
-            const uint32_t c = (*reinterpret_cast<const uint32_t *>(p + row * 4) >> (8 * (s & 3))) & 255u;
-            return __uint_as_float(c == 0 ? 0x00400000u : c == 255 ? 0x7FC00000u : c << 23);
-        }
-        return *reinterpret_cast<const float *>(p + (a.s_row == 1 ? row * 4 + (s & 3) * (MT * 4) : row * 16 + (s & 3) * 4));
+        const uint32_t p = lds0 + S::kScales + (batch % kScaleRing) * S::kScaleBatch;
+        const uint32_t row = (uint32_t)((wm * MF + m) * 16 + (lane & 15));
+        // a row's four words side by side, four rows of words, or one word a row
+        const uint32_t at = p + row * (a.s_row != 1 && !a.s_packed ? 16u : 4u) +
+                            (uint32_t)(s & 3) * (a.s_packed ? 0u : a.s_row == 1 ? MT * 4u : 4u);
+        const uint32_t w = *(__attribute__((address_space(3))) const uint32_t *)(uintptr_t)at;
+        const uint32_t c = (w >> (8 * (s & 3))) & 255u;
+        const uint32_t e = c == 0 ? 0x00400000u : c == 255 ? 0x7FC00000u : c << 23;
+        return __uint_as_float(a.s_packed ? e : w);
     }
     // of the wave's weight rows (SwiGLU: up = 0, 1 its gate, up rows)
     __device__ __forceinline__ float weight_scale(int s, int up) const
@@ -456,13 +491,37 @@ struct ProductWg {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, u), __builtin_bit_cast(v8bf16, v), c, 0, 0, 0);
     }
 
+    // Share of `total` items that follows instruction i of `of`.
+    template <typename F>
+    static __device__ __forceinline__ void share(int i, int of, int total, F &&f)
+    {
+#pragma unroll
+        for (int x = 0; x < total; ++x)
+            if (x * of / total == i) f(x);
+    }
+
+    // fp8: the waiting sums of A fragment n into acc.
+    __device__ __forceinline__ void add_part(int n, int m)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(part[m][i], part_s[m], acc[n][m][i]);
+        // here, not where the compiler would gather the additions of all fragments (whose sums then fill the registers)
+        asm volatile("" : "+v"(acc[n][m]));
+    }
+
     // Stage s of the tile, in LDS buffer buf, its first fragments in registers;
     // leaves the next stage's there and loads a stage into buf.
+    //
+    // The order is fixed by hand: every matrix instruction is followed by a
+    // share of the other work.  The barrier stands where the last A fragments of
+    // the stage are in registers; behind it the buffer is free for the loads of
+    // stage s + kBufs, and the next stage's fragments are read.  fp8: the sums
+    // of a stage are scaled and added while the next fragment's are under way.
     template <bool BUSY, typename F>
     __device__ __forceinline__ void run_stage(int buf, int s, F &&next)
     {
         const int nbuf = buf + 1 == S::kBufs ? 0 : buf + 1;
-        constexpr int kLeft = (S::kBufs - 2) * (S::kAUnits + S::kBUnits);
+        constexpr int kLeft = (S::kBufs - 2) * S::kUnits;
         if constexpr (!BUSY) {
             sync_stage<kLeft>();
             load_next(buf, next);
@@ -478,36 +537,30 @@ struct ProductWg {
                     sc2[m] = real && EPI != kPlain ? t * u : 0.0f;
                 }
             }
+            Units u;
+            constexpr int kPer = FP8 ? MF : 2 * MF, kAfter = D * kPer;       // matrix instructions per fragment, after the barrier
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 if (n == NF - D) {
                     sync_stage<kLeft>();
-                    fa[(n + D) % R] = a_fragment(nbuf, (n + D) % NF);
-                    load_next(buf, next);
-                } else {
-                    fa[(n + D) % R] = a_fragment(n + D < NF ? buf : nbuf, (n + D) % NF);
+                    u = begin_load(buf, next);
                 }
-                if constexpr (FP8) {
-                    f32x4 p[MF];
+                fa[(n + D) % R] = a_fragment(n + D < NF ? buf : nbuf, (n + D) % NF);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        p[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[n % R], fb[m], f32x4{}, 0, 0, 0, 0, 0, 0);
-                        if (n == NF - 1) fb[m] = b_fragment(nbuf, m);
+                for (int x = 0; x < kPer; ++x) {
+                    const int m = x % MF;
+                    if constexpr (FP8) {
+                        add_part((n + NF - 1) % NF, m);
+                        part[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[n % R], fb[m], f32x4{}, 0, 0, 0, 0, 0, 0);
+                        part_s[m] = EPI != kPlain && n >= NF / 2 ? sc2[m] : sc[m];
+                    } else {
+                        acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], x / MF);
                     }
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        const float f = EPI != kPlain && n >= NF / 2 ? sc2[m] : sc[m];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(p[m][i], f, acc[n][m][i]);
-                    }
-                } else {
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], 0);
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], 1);
-                        if (n == NF - 1) fb[m] = b_fragment(nbuf, m);
-                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (n == NF - 1 && x >= kPer - MF) fb[m] = b_fragment(nbuf, m);
+                    if (n >= NF - D) share((n - (NF - D)) * kPer + x, kAfter, S::kUnits, [&](int j) { load_unit(u, j); });
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -526,12 +579,20 @@ struct ProductWg {
 #pragma unroll
             for (int j = 0; j < D; ++j) fa[j] = a_fragment(buf, j);
 #pragma unroll
-            for (int j = 0; j < MF; ++j) fb[j] = b_fragment(buf, j);
+            for (int j = 0; j < MF; ++j) {
+                fb[j] = b_fragment(buf, j);
+                part[j] = f32x4{};
+                part_s[j] = 0.0f;
+            }
         }
         for (int s = 0; s < stages; ++s) {
             run_stage<BUSY>(buf, s, next);
             if (FP8 && ((s & 3) == 3 || s == stages - 1)) ++batch;
             buf = buf + 1 == S::kBufs ? 0 : buf + 1;
+        }
+        if constexpr (BUSY && FP8) {
+#pragma unroll
+            for (int m = 0; m < MF; ++m) add_part(NF - 1, m);
         }
         return buf;
     }
@@ -760,7 +821,7 @@ __global__ __launch_bounds__(kProductThreads) void product_kernel(ProductArgs a,
     w.set_tile(tile());
     w.load_stage = 0;
     for (int b = 0; b < S::kBufs; ++b) w.load_next(b, next);
-    sync_stage<(S::kBufs - 1) * (S::kAUnits + S::kBUnits)>();
+    sync_stage<(S::kBufs - 1) * S::kUnits>();
     int buf = 0;
     for (int32_t at = id; at < last; at += step) {
         w.take_tile();
