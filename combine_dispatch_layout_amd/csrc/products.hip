@@ -433,33 +433,40 @@ struct ProductWg {
     // fragment f of the wave's, from the buffer that begins at `at`; by rows
     // the two chunks are 64 bytes apart, swizzled
     template <bool COLS>
-    __device__ __forceinline__ i32x8 fragment(uint32_t at, uint32_t of_lane, int f) const
+    __device__ __forceinline__ u32x4 half_fragment(uint32_t at, uint32_t of_lane, int f, int half) const
     {
-        u32x4 lo, hi;
         if constexpr (COLS) {
-            const uint32_t p = at + (of_lane ^ (uint32_t)(f << 5));
+            const uint32_t p = at + (of_lane ^ (uint32_t)(f << 5)) + (uint32_t)half * (32 * 512);
             auto tr = [&](int q) {
                 using lds_i16x4 = __attribute__((address_space(3))) i16x4;
                 return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(p + q * 512)));
             };
-            const u32x2 a0 = tr(0), a1 = tr(4), b0 = tr(32), b1 = tr(36);
-            lo = u32x4{a0.x, a0.y, a1.x, a1.y};
-            hi = u32x4{b0.x, b0.y, b1.x, b1.y};
+            const u32x2 x = tr(0), y = tr(4);
+            return u32x4{x.x, x.y, y.x, y.y};
         } else {
             using lds_u32x4 = __attribute__((address_space(3))) const u32x4;
-            lo = *(lds_u32x4 *)(uintptr_t)(at + of_lane + f * (16 * kLine));
-            hi = *(lds_u32x4 *)(uintptr_t)(at + (of_lane ^ 64) + f * (16 * kLine));
+            return *(lds_u32x4 *)(uintptr_t)(at + (of_lane ^ (uint32_t)(half * 64)) + f * (16 * kLine));
         }
+    }
+    static __device__ __forceinline__ i32x8 join(const u32x4 &lo, const u32x4 &hi)
+    {
         return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    }
+    static __device__ __forceinline__ u32x4 half_of(const i32x8 &x, int half)
+    {
+        return half ? u32x4{(uint32_t)x[4], (uint32_t)x[5], (uint32_t)x[6], (uint32_t)x[7]}
+                    : u32x4{(uint32_t)x[0], (uint32_t)x[1], (uint32_t)x[2], (uint32_t)x[3]};
     }
     __device__ __forceinline__ i32x8 a_fragment(int buf, int n) const
     {
-        return fragment<S::kACols>(lds0 + (uint32_t)buf * S::kBuf, a_lane, n);
+        const uint32_t at = lds0 + (uint32_t)buf * S::kBuf;
+        return join(half_fragment<S::kACols>(at, a_lane, n, 0), half_fragment<S::kACols>(at, a_lane, n, 1));
     }
-    __device__ __forceinline__ i32x8 b_fragment(int buf, int m) const
+    __device__ __forceinline__ u32x4 b_half(int buf, int m, int half) const
     {
-        return fragment<S::kBCols>(lds0 + (uint32_t)buf * S::kBuf + kProductNT * kLine, b_lane, m);
+        return half_fragment<S::kBCols>(lds0 + (uint32_t)buf * S::kBuf + kProductNT * kLine, b_lane, m, half);
     }
+    __device__ __forceinline__ i32x8 b_fragment(int buf, int m) const { return join(b_half(buf, m, 0), b_half(buf, m, 1)); }
 
     // fp8: scale of the lane's row of fragment m in stage s of the batch in use
     __device__ __forceinline__ float token_scale(int s, int m) const
@@ -484,11 +491,8 @@ struct ProductWg {
 
     static __device__ __forceinline__ f32x4 mma(const i32x8 &x, const i32x8 &y, f32x4 c, int half)
     {
-        const u32x4 u = half ? u32x4{(uint32_t)x[4], (uint32_t)x[5], (uint32_t)x[6], (uint32_t)x[7]}
-                             : u32x4{(uint32_t)x[0], (uint32_t)x[1], (uint32_t)x[2], (uint32_t)x[3]};
-        const u32x4 v = half ? u32x4{(uint32_t)y[4], (uint32_t)y[5], (uint32_t)y[6], (uint32_t)y[7]}
-                             : u32x4{(uint32_t)y[0], (uint32_t)y[1], (uint32_t)y[2], (uint32_t)y[3]};
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, u), __builtin_bit_cast(v8bf16, v), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, half_of(x, half)),
+                                                       __builtin_bit_cast(v8bf16, half_of(y, half)), c, 0, 0, 0);
     }
 
     // Share of `total` items that follows instruction i of `of`.
@@ -558,7 +562,13 @@ struct ProductWg {
                         acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], x / MF);
                     }
                     __builtin_amdgcn_sched_barrier(0);
-                    if (n == NF - 1 && x >= kPer - MF) fb[m] = b_fragment(nbuf, m);
+                    // B's registers take the next stage's as soon as they are used up
+                    if (n == NF - 1) {
+                        if constexpr (FP8)
+                            fb[m] = b_fragment(nbuf, m);
+                        else
+                            fb[m] = x < MF ? join(b_half(nbuf, m, 0), half_of(fb[m], 1)) : join(half_of(fb[m], 0), b_half(nbuf, m, 1));
+                    }
                     if (n >= NF - D) share((n - (NF - D)) * kPer + x, kAfter, S::kUnits, [&](int j) { load_unit(u, j); });
                     __builtin_amdgcn_sched_barrier(0);
                 }
