@@ -418,12 +418,11 @@ struct GroupedArgs {
     uint8_t *hs;
 };
 
-// Expert e's first row and its row count, held inside the buffer whatever
-// the device arrays say.
+// An expert's first row b and row count c, held inside the buffer whatever the
+// device arrays say.
 template <typename Args>
-__device__ __forceinline__ int64_t grouped_rows(const Args &a, int e, int64_t *begin, bool *bad)
+__device__ __forceinline__ int64_t held_rows(const Args &a, int64_t c, int64_t b, int64_t *begin, bool *bad)
 {
-    int64_t c = a.counts[e], b = a.seg ? a.seg[e] : (int64_t)e * a.cap;
     const int64_t most = a.seg ? a.rows : a.cap;
     *bad = c < 0 || b < 0;
     if (c < 0) c = 0;
@@ -433,6 +432,11 @@ __device__ __forceinline__ int64_t grouped_rows(const Args &a, int e, int64_t *b
     if (c > a.rows - b) { c = a.rows - b; *bad = true; }
     *begin = b;
     return c;
+}
+template <typename Args>
+__device__ __forceinline__ int64_t grouped_rows(const Args &a, int e, int64_t *begin, bool *bad)
+{
+    return held_rows(a, a.counts[e], a.seg ? a.seg[e] : (int64_t)e * a.cap, begin, bad);
 }
 
 struct GroupedTile {
@@ -469,17 +473,15 @@ __device__ __forceinline__ int32_t grouped_tile_table(const Args &a, int tiles_n
     return base;
 }
 
-// Tile `id` of the table: tiles are ordered by expert, then column tile, then
-// row tile (the row tiles of one weight tile run side by side, so its second
-// reader finds it in a cache).
-template <typename Args>
-__device__ __forceinline__ GroupedTile grouped_tile(const Args &a, const int32_t *ends, int tiles_n, int32_t id)
+// Place of tile `id` in the table: tiles are ordered by expert, then column
+// tile, then row tile (the row tiles of one weight tile run side by side, so
+// its second reader finds it in a cache).
+__device__ __forceinline__ void grouped_place(GroupedTile &t, const int32_t *ends, int L, int tiles_n, int32_t id)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    GroupedTile t;
     t.e = 0;
-    for (int e0 = 0; e0 < a.L; e0 += kWave) {
-        const bool before = e0 + lane < a.L && ends[e0 + lane] <= id;
+    for (int e0 = 0; e0 < L; e0 += kWave) {
+        const bool before = e0 + lane < L && ends[e0 + lane] <= id;
         const int n = __popcll(__ballot(before));
         t.e += n;
         if (n < kWave) break;
@@ -489,6 +491,12 @@ __device__ __forceinline__ GroupedTile grouped_tile(const Args &a, const int32_t
     const int32_t mt = (ends[t.e] - from) / tiles_n, local = id - from;
     t.n = __builtin_amdgcn_readfirstlane(local / mt);
     t.m = __builtin_amdgcn_readfirstlane(local % mt);
+}
+template <typename Args>
+__device__ __forceinline__ GroupedTile grouped_tile(const Args &a, const int32_t *ends, int tiles_n, int32_t id)
+{
+    GroupedTile t;
+    grouped_place(t, ends, a.L, tiles_n, id);
     bool bad;
     t.count = grouped_rows(a, t.e, &t.begin, &bad);
     return t;

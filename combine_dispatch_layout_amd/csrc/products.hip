@@ -103,7 +103,7 @@ constexpr int kProductThreads = 512;
 constexpr int kProductNT = 256;          // A of a tile
 constexpr int kProductWgs = 256;         // one per CU
 constexpr int kLine = 128;               // bytes of a row per stage: 64 bf16, or the 128 elements of an fp8 scale
-constexpr int kScaleRing = 4;            // batches (four stages' scales) in LDS
+constexpr int kScaleRing = 3;            // batches (four stages' scales) in LDS: in use, loaded, and being left
 constexpr uint32_t kFar = 0x80000000u;   // no tile operand reaches this offset: loads there read no memory and give zeros
 
 __device__ __forceinline__ uint32_t lds_address(const uint8_t *p)
@@ -118,11 +118,13 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t *p)
 // zeros.  M0 holds the LDS address; nothing else here uses it.
 __device__ __forceinline__ void dma16(u32x4 r, uint32_t off, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(to));
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r),
+                 "s"(__builtin_amdgcn_readfirstlane((int)to)));
 }
 __device__ __forceinline__ void dma4(u32x4 r, uint32_t off, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(to));
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(r),
+                 "s"(__builtin_amdgcn_readfirstlane((int)to)));
 }
 // (the values are the same in all lanes)
 __device__ __forceinline__ u32x4 scalar_rsrc(const uint8_t *base, uint32_t bytes)
@@ -152,19 +154,26 @@ __device__ __forceinline__ void swap_rows16(uint32_t &a, uint32_t &b)
 
 template <bool FP8, ProductForm FORM, int MT>
 struct ProductShape {
-    static constexpr int WN = MT == 256 ? 2 : 4;
-    // wave w has A part w % WN and B part w / WN: the two waves of a SIMD
-    // (w, w + 4) are in different halves of B, so a tile that is half full keeps
-    // every SIMD busy
-    static constexpr int WM = 8 / WN;
+    // 8 waves, 2 parts of A by 4 of B: wave w has A's half w % 2, and of B's blocks
+    // of 16 rows every fourth from w / 2 on, so that a tile's live rows are spread
+    // evenly over the waves.
+    static constexpr int WN = 2, WM = 4;
     static constexpr int NF = kProductNT / 16 / WN;      // 16-row fragments per wave
     static constexpr int MF = MT / 16 / WM;
     static constexpr bool kACols = FORM != kFwd, kBCols = FORM == kDw;
-    static constexpr int kBufs = MT == 256 ? 2 : 3;
-    static constexpr int kBuf = (kProductNT + MT) * kLine;
-    static constexpr int kAUnits = 4, kUnits = 4 + MT / 64;   // loads per wave and stage (of A first)
-    static constexpr int kScaleBatch = MT * 16 + 1024;   // token scales, then the weights'
-    static constexpr int kScales = kBufs * kBuf;
+    // stages of each operand in LDS: what is multiplied, and one or two on their way
+    static constexpr int kABufs = MT == 256 ? 2 : 3, kBBufs = MT >= 192 ? 2 : 3;
+    static constexpr int kABuf = kProductNT * kLine, kBBuf = MT * kLine;
+    static constexpr int kBBase = kABufs * kABuf;
+    static constexpr int kMinStages = kABufs;
+    // Loads per wave and stage, B's first.  When stage s + 1 has to be there, what
+    // was loaded behind its A (of stage s + 1 - kABufs on) and behind its B may be
+    // under way.
+    static constexpr int kAUnits = 4, kBUnits = MT / 64, kUnits = kAUnits + kBUnits;
+    static constexpr int kLeftA = (kABufs - 1) * kBUnits + (kABufs - 2) * kAUnits, kLeftB = (kBBufs - 1) * kUnits;
+    static constexpr int kLeft = kLeftA < kLeftB ? kLeftA : kLeftB;
+    static constexpr int kScaleBatch = MT * 16 + 256;    // token scales, then the weights'
+    static constexpr int kScales = kBBase + kBBufs * kBBuf;
     static constexpr int kAmax = kScales + (FP8 ? kScaleRing * kScaleBatch : 0);
     static constexpr size_t kLds = kAmax + (FP8 ? WN * MT * 4 : 0);   // then the tile table
 };
@@ -179,6 +188,14 @@ struct ProductSide {
     uint32_t off;                // the lane's offset in unit 0 of stage 0
 };
 
+// A tile of the output.
+struct TileAt {
+    int64_t row0, n0;            // its first row (kDw: of the expert's weights) and column
+    int64_t begin, count;        // the expert's rows
+    int64_t m0;                  // the tile's first of them
+    int e, live_m, live_n, stages;
+};
+
 template <bool FP8, ProductForm FORM, ProductEpilogue EPI, int MT>
 struct ProductWg {
     using S = ProductShape<FP8, FORM, MT>;
@@ -186,34 +203,41 @@ struct ProductWg {
     static constexpr int NF = S::NF, MF = S::MF;
     static constexpr int R = FP8 ? 2 : 4, D = R - 1;           // fragments of A in registers, read ahead
     static_assert(NF % R == 0, "a fragment's registers do not depend on the stage");
-    static constexpr bool kUpByUnit = EPI != kPlain && S::WN == 2, kUpByHalf = EPI != kPlain && S::WN == 4;
+    static constexpr bool kUpByUnit = EPI != kPlain;           // A's units alternate between gate and up rows
 
     const ProductArgs a;
+    const int32_t *const ends;
+    const int tiles_m, tiles_n;
+    const int32_t last, step;                // the workgroup's tiles
     uint8_t *const lds;
     const int tid, lane, wave, wn, wm;
     const uint32_t lds0;                     // LDS address of the buffers
     const uint32_t a_lane, b_lane;           // a lane's place in the wave's first fragments
     // operands being loaded
     ProductSide sa, sb;
-    int load_stage, load_stages;
+    int32_t id_a, id_b;                      // tile, stage and stages that each operand loads next
+    int stage_a, stages_a, stage_b, stages_b;
     const uint8_t *tok_s, *w_s;              // fp8: the tile's scales
     int live_rows, live_blocks;              // rows with scales; weight scale blocks
     uint32_t load_batch, batch;              // ring positions
-    // the tile being multiplied
-    int64_t row0, n0, begin;
-    int live_m, live_n, e, stages;
-    int64_t next_row0, next_n0, next_begin;
-    int next_live_m, next_live_n, next_e, next_stages;
+    int buf_a, buf_b;                        // buffers of the stage being multiplied
+    TileAt at, at_b, known;                  // the tile being multiplied, B's, the one described last
+    int32_t known_id;
 
-    f32x4 acc[NF][MF];
-    i32x8 fa[R], fb[MF];
-    f32x4 part[MF];                          // fp8: the sums of a stage of the A fragment before, and their scales
-    float part_s[MF];
+    // A tile under way, M fragments of B a wave.
+    template <int M>
+    struct Work {
+        f32x4 acc[NF][M];
+        i32x8 fa[R], fb[M];
+        f32x4 part[M];                       // fp8: the sums of a stage of the A fragment before, and their scales
+        float part_s[M];
+    };
 
-    __device__ __forceinline__ ProductWg(const ProductArgs &args, uint8_t *l)
-        : a(args), lds(l), tid(threadIdx.x), lane(tid & (kWave - 1)), wave(wave_id()), wn(wave % S::WN), wm(wave / S::WN),
-          lds0(lds_address(l)), a_lane(fragment_lane<S::kACols>(wn * S::NF)), b_lane(fragment_lane<S::kBCols>(wm * S::MF)),
-          load_batch(0), batch(0)
+    __device__ __forceinline__ ProductWg(const ProductArgs &args, uint8_t *l, const int32_t *e, int tm, int tn, int32_t end,
+                                         int32_t every)
+        : a(args), ends(e), tiles_m(tm), tiles_n(tn), last(end), step(every), lds(l), tid(threadIdx.x), lane(tid & (kWave - 1)), wave(wave_id()), wn(wave % S::WN), wm(wave / S::WN),
+          lds0(lds_address(l)), a_lane(fragment_lane<S::kACols>(wn * S::NF)), b_lane(fragment_lane<S::kBCols>(wm)),
+          load_batch(0), batch(0), buf_a(0), buf_b(0), known_id(-1)
     {
     }
 
@@ -233,12 +257,12 @@ struct ProductWg {
         return (uint32_t)((lane & 31) ^ (((d & 3) | (d >> 3 & 1) << 2) << 1));
     }
 
-    __device__ __forceinline__ void side_by_rows(ProductSide &s, const uint8_t *p, int64_t ld, int live, int half_rows)
+    __device__ __forceinline__ void side_by_rows(ProductSide &s, const uint8_t *p, int64_t ld, int live)
     {
         s.p = p;
         s.ld = (uint32_t)ld;
         s.bytes = (uint32_t)live * s.ld;
-        s.off = (uint32_t)((half_rows ? (wave & 3) : wave) * 8 + (lane >> 3)) * s.ld + row_chunk() * 16;
+        s.off = (uint32_t)(wave * 8 + (lane >> 3)) * s.ld + row_chunk() * 16;
     }
     __device__ __forceinline__ void side_by_columns(ProductSide &s, const uint8_t *p, int64_t ld, int64_t depth, int64_t first)
     {
@@ -252,7 +276,7 @@ struct ProductWg {
     // The loads of one stage, unit by unit.
     struct Units {
         u32x4 ra, ra2, rb;
-        uint32_t a_off, b_off, to;
+        uint32_t a_off, b_off, a_to, b_to;
     };
     template <bool COLS>
     __device__ __forceinline__ u32x4 side_rsrc(const ProductSide &s, const uint8_t *p, int stage) const
@@ -274,15 +298,15 @@ struct ProductWg {
             return k + row_chunk() * 16 < s.ld ? s.off + k : kFar;
         }
     }
-    __device__ __forceinline__ void load_unit(Units &u, int j) const
+    __device__ __forceinline__ void load_b(Units &u, int j) const
     {
-        if (j < S::kAUnits) {
-            dma16(kUpByUnit && (j & 1) ? u.ra2 : u.ra, u.a_off, u.to + j * 8192);
-            if (!kUpByUnit || (j & 1)) u.a_off += (S::kACols ? 16 : kUpByHalf ? 32 : 64) * sa.ld;
-        } else {
-            dma16(u.rb, u.b_off, u.to + j * 8192);
-            u.b_off += (S::kBCols ? 16 : 64) * sb.ld;
-        }
+        dma16(u.rb, u.b_off, u.b_to + j * 8192);
+        u.b_off += (S::kBCols ? 16 : 64) * sb.ld;
+    }
+    __device__ __forceinline__ void load_a(Units &u, int j) const
+    {
+        dma16(kUpByUnit && (j & 1) ? u.ra2 : u.ra, u.a_off, u.a_to + j * 8192);
+        if (!kUpByUnit || (j & 1)) u.a_off += (S::kACols ? 16 : 64) * sa.ld;
     }
 
     // The scales of stages 4 q to 4 q + 3: a row's four words (or the word that
@@ -314,101 +338,155 @@ struct ProductWg {
             const int64_t G = a.K / 128;
             const uint32_t step = (uint32_t)(EPI == kPlain ? G : a.N / 256 * G) * 4;
             const uint32_t bytes = live_blocks == 0 ? 0u : (uint32_t)((live_blocks - 1) * (int64_t)step + G * 4) - (uint32_t)q * 16;
-            dma16(scalar_rsrc(w_s + (int64_t)q * 16, bytes), lane < 2 ? (uint32_t)lane * step : kFar, to + MT * 16);
+            // lane 4 b + g: block b's scale of group g
+            dma4(scalar_rsrc(w_s + (int64_t)q * 16, bytes), lane < 8 ? (uint32_t)(lane >> 2) * step + (uint32_t)(lane & 3) * 4 : kFar,
+                 to + MT * 16);
         }
         ++load_batch;
     }
 
-    // Begins the loads of the next stage in order to buffer `buf`; next() moves
-    // to the next tile.
-    template <typename F>
-    __device__ __forceinline__ Units begin_load(int buf, F &&next)
+    // Begins the loads of each operand's next stage, A's to its buffer buf_a and
+    // B's to buf_b.
+    __device__ __forceinline__ void begin_b(Units &u, int buf)
     {
-        if (load_stage == load_stages) {
-            next();
-            load_stage = 0;
+        if (stage_b == stages_b) {
+            id_b += step;
+            set_b();
         }
-        if (FP8 && (load_stage & 3) == 0) load_scales(load_stage >> 2);
-        Units u;
-        u.ra = side_rsrc<S::kACols>(sa, kUpByHalf && wave >= 4 ? sa.p2 : sa.p, load_stage);
-        if (kUpByUnit) u.ra2 = side_rsrc<S::kACols>(sa, sa.p2, load_stage);
-        u.rb = side_rsrc<S::kBCols>(sb, sb.p, load_stage);
-        u.a_off = side_off<S::kACols>(sa, load_stage);
-        u.b_off = side_off<S::kBCols>(sb, load_stage);
-        u.to = lds0 + (uint32_t)buf * S::kBuf + (uint32_t)wave * 1024;
-        ++load_stage;
-        return u;
+        if (FP8 && (stage_b & 3) == 0) load_scales(stage_b >> 2);
+        u.rb = side_rsrc<S::kBCols>(sb, sb.p, stage_b);
+        u.b_off = side_off<S::kBCols>(sb, stage_b);
+        u.b_to = lds0 + S::kBBase + (uint32_t)buf * S::kBBuf + (uint32_t)wave * 1024;
+        ++stage_b;
     }
-    template <typename F>
-    __device__ __forceinline__ void load_next(int buf, F &&next)
+    __device__ __forceinline__ void begin_a(Units &u, int buf)
     {
-        Units u = begin_load(buf, next);
+        if (stage_a == stages_a) {
+            id_a += step;
+            set_a();
+        }
+        u.ra = side_rsrc<S::kACols>(sa, sa.p, stage_a);
+        if (kUpByUnit) u.ra2 = side_rsrc<S::kACols>(sa, sa.p2, stage_a);
+        u.a_off = side_off<S::kACols>(sa, stage_a);
+        u.a_to = lds0 + (uint32_t)buf * S::kABuf + (uint32_t)wave * 1024;
+        ++stage_a;
+    }
+    __device__ __forceinline__ void load_all_b(int buf)
+    {
+        Units u;
+        begin_b(u, buf);
 #pragma unroll
-        for (int j = 0; j < S::kUnits; ++j) load_unit(u, j);
+        for (int j = 0; j < S::kBUnits; ++j) load_b(u, j);
+    }
+    __device__ __forceinline__ void load_all_a(int buf)
+    {
+        Units u;
+        begin_a(u, buf);
+#pragma unroll
+        for (int j = 0; j < S::kAUnits; ++j) load_a(u, j);
+    }
+    // Before the first tile: everything but what the first stage's turn loads.
+    __device__ __forceinline__ void start(int32_t id)
+    {
+        id_a = id_b = id;
+        set_b();
+        set_a();
+#pragma unroll
+        for (int x = 0; x < S::kABufs; ++x) {
+            if (x < S::kBBufs) load_all_b(x);
+            load_all_a(x);
+        }
+        // the first stage of both
+        sync_stage<(S::kBBufs - 1) * S::kUnits + (S::kABufs - S::kBBufs) * S::kAUnits>();
     }
 
-    // Sets what is loaded to tile `id`.
-    __device__ __forceinline__ void set_tile(const GroupedTile &t)
+    // Tile `id`.  Both operands ask for it, one after the other; the second time
+    // it is known.  Tiles of the weights' gradient run over the experts, each with
+    // tiles_m x tiles_n of them whatever its count.
+    __device__ __forceinline__ TileAt describe(int32_t id)
     {
-        const int64_t eb = FP8 ? 1 : 2;
-        next_e = t.e;
-        next_begin = t.begin;
-        next_n0 = (int64_t)t.n * kCols;
+        if (id == known_id) return known;
+        known_id = id;
+        GroupedTile g;
         if constexpr (FORM == kDw) {
-            next_row0 = (int64_t)t.m * MT;                   // a row of the weights
-            next_live_m = (int)(a.N - next_row0 < MT ? a.N - next_row0 : MT);
-            next_live_n = (int)(a.K - next_n0 < kCols ? a.K - next_n0 : kCols);
-            next_stages = (int)((t.count + 63) / 64);
-            side_by_columns(sa, a.a + t.begin * a.K * 2, a.K * 2, t.count, next_n0);
-            side_by_columns(sb, a.b + t.begin * a.N * 2, a.N * 2, t.count, next_row0);
+            const int32_t per = tiles_m * tiles_n, local = id % per;
+            g.e = id / per;
+            g.n = local / tiles_m;
+            g.m = local % tiles_m;
         } else {
-            const int64_t m0 = (int64_t)t.m * MT;
-            next_row0 = t.begin + m0;
-            next_live_m = (int)(t.count - m0 < MT ? t.count - m0 : MT);
-            if constexpr (FORM == kDx) {
-                next_live_n = (int)(a.K - next_n0 < kCols ? a.K - next_n0 : kCols);
-                next_stages = (int)((a.N * 2 + kLine - 1) / kLine);
-                side_by_columns(sa, a.a + (int64_t)t.e * a.N * a.K * 2, a.K * 2, a.N, next_n0);
-                side_by_rows(sb, a.b + next_row0 * a.N * 2, a.N * 2, next_live_m, false);
-            } else {
-                const int64_t width = EPI == kPlain ? a.N : a.N / 2;
-                next_live_n = (int)(width - next_n0 < kCols ? width - next_n0 : kCols);
-                next_stages = (int)((a.K * eb + kLine - 1) / kLine);
-                const uint8_t *w = a.a + ((int64_t)t.e * a.N + next_n0) * a.K * eb;
-                side_by_rows(sa, w, a.K * eb, next_live_n, kUpByHalf);
-                sa.p2 = w + width * a.K * eb;
-                side_by_rows(sb, a.b + next_row0 * a.K * eb, a.K * eb, next_live_m, false);
-                if constexpr (FP8) {
-                    const int64_t G = a.K / 128, NB = (a.N + 127) / 128;
-                    const int64_t blk = next_n0 / 128;
-                    w_s = reinterpret_cast<const uint8_t *>(a.a_s + ((int64_t)t.e * NB + blk) * G);
-                    live_blocks = EPI != kPlain || NB - blk > 1 ? 2 : 1;
-                    live_rows = next_live_m;
-                    tok_s = a.b_s + 4 * (a.s_mat ? t.e * a.s_mat + m0 : next_row0 * a.s_row);
-                }
-            }
+            grouped_place(g, ends, a.L, tiles_n, id);
         }
-        // one buffer's stages at least (empty ones read no memory): what is loaded is one tile ahead at most
-        if (next_stages < S::kBufs) next_stages = S::kBufs;
-        load_stages = next_stages;
+        // scalar loads: nothing writes these arrays meanwhile
+        using scalar_i32 = __attribute__((address_space(4))) const int32_t;
+        using scalar_i64 = __attribute__((address_space(4))) const int64_t;
+        const int64_t c = ((scalar_i32 *)(uintptr_t)a.counts)[g.e];
+        const int64_t first = a.seg ? ((scalar_i64 *)(uintptr_t)a.seg)[g.e] : (int64_t)g.e * a.cap;
+        bool bad;
+        g.count = held_rows(a, c, first, &g.begin, &bad);
+        TileAt t;
+        t.e = g.e;
+        t.begin = g.begin;
+        t.count = g.count;
+        if constexpr (FORM == kDw) {
+            t.m0 = (int64_t)g.m * MT;
+            t.live_m = (int)(a.N - t.m0 < MT ? a.N - t.m0 : MT);
+        } else {
+            // An expert's row tiles share its rows evenly: workgroups that read the same weights keep step, so
+            // that all but the first find them in the L2.  131072 rows of 128 experts, K = N = 4096: full tiles and
+            // a rest 51% of the requests, 4.25 ms; evenly in blocks of 64 rows 4.15 ms; evenly 76%, 4.02 ms.
+            const int c = (int)g.count, mt = (c + MT - 1) / MT, q = c / mt, more = c - q * mt;
+            t.m0 = (int64_t)g.m * q + (g.m < more ? g.m : more);
+            t.live_m = q + (g.m < more ? 1 : 0);
+        }
+        t.n0 = (int64_t)g.n * kCols;
+        t.row0 = FORM == kDw ? t.m0 : t.begin + t.m0;
+        const int64_t cols = (FORM != kFwd ? a.K : EPI == kPlain ? a.N : a.N / 2) - t.n0;
+        t.live_n = (int)(cols < kCols ? cols : kCols);
+        t.stages = FORM == kFwd  ? (int)((a.K * (FP8 ? 1 : 2) + kLine - 1) / kLine)
+                   : FORM == kDx ? (int)((a.N * 2 + kLine - 1) / kLine)
+                                 : (int)((t.count + 63) / 64);
+        // empty stages (which read no memory) up to the number of buffers: what is loaded is one tile ahead at most
+        if (t.stages < S::kMinStages) t.stages = S::kMinStages;
+        known = t;
+        return t;
     }
-    // No tile to load: the operands are empty.
-    __device__ __forceinline__ void set_no_tile()
+    // Moves an operand to its next tile; past the last it is empty.
+    __device__ __forceinline__ void set_a()
     {
-        sa.bytes = sb.bytes = 0;
-        sa.depth = sb.depth = 0;
-        live_rows = live_blocks = 0;
-        load_stages = INT32_MAX;
+        const bool none = id_a >= last;
+        const TileAt t = describe(none ? last - 1 : id_a);
+        stage_a = 0;
+        stages_a = none ? INT32_MAX : t.stages;
+        if constexpr (FORM == kDw) {
+            side_by_columns(sa, a.a + t.begin * a.K * 2, a.K * 2, none ? 0 : t.count, t.n0);
+        } else if constexpr (FORM == kDx) {
+            side_by_columns(sa, a.a + (int64_t)t.e * a.N * a.K * 2, a.K * 2, none ? 0 : a.N, t.n0);
+        } else {
+            const int64_t row = a.K * (FP8 ? 1 : 2);
+            side_by_rows(sa, a.a + ((int64_t)t.e * a.N + t.n0) * row, row, none ? 0 : t.live_n);
+            sa.p2 = sa.p + a.N / 2 * row;
+        }
     }
-    __device__ __forceinline__ void take_tile()
+    __device__ __forceinline__ void set_b()
     {
-        row0 = next_row0;
-        n0 = next_n0;
-        begin = next_begin;
-        live_m = next_live_m;
-        live_n = next_live_n;
-        e = next_e;
-        stages = next_stages;
+        const bool none = id_b >= last;
+        const TileAt t = describe(none ? last - 1 : id_b);
+        at_b = t;
+        stage_b = 0;
+        stages_b = none ? INT32_MAX : t.stages;
+        if constexpr (FORM == kDw) {
+            side_by_columns(sb, a.b + t.begin * a.N * 2, a.N * 2, none ? 0 : t.count, t.row0);
+        } else {
+            const int64_t row = FORM == kDx ? a.N * 2 : a.K * (FP8 ? 1 : 2);
+            side_by_rows(sb, a.b + t.row0 * row, row, none ? 0 : t.live_m);
+        }
+        if constexpr (FP8) {
+            const int64_t G = a.K / 128, NB = (a.N + 127) / 128, blk = t.n0 / 128;
+            w_s = reinterpret_cast<const uint8_t *>(a.a_s + ((int64_t)t.e * NB + blk) * G);
+            live_blocks = none ? 0 : EPI != kPlain || NB - blk > 1 ? 2 : 1;
+            live_rows = none ? 0 : t.live_m;
+            tok_s = a.b_s + 4 * (a.s_mat ? t.e * a.s_mat + t.m0 : t.row0 * a.s_row);
+        }
     }
 
     // ---- fragments ----
@@ -459,12 +537,12 @@ struct ProductWg {
     }
     __device__ __forceinline__ i32x8 a_fragment(int buf, int n) const
     {
-        const uint32_t at = lds0 + (uint32_t)buf * S::kBuf;
+        const uint32_t at = lds0 + (uint32_t)buf * S::kABuf;
         return join(half_fragment<S::kACols>(at, a_lane, n, 0), half_fragment<S::kACols>(at, a_lane, n, 1));
     }
     __device__ __forceinline__ u32x4 b_half(int buf, int m, int half) const
     {
-        return half_fragment<S::kBCols>(lds0 + (uint32_t)buf * S::kBuf + kProductNT * kLine, b_lane, m, half);
+        return half_fragment<S::kBCols>(lds0 + S::kBBase + (uint32_t)buf * S::kBBuf, b_lane, m * S::WM, half);
     }
     __device__ __forceinline__ i32x8 b_fragment(int buf, int m) const { return join(b_half(buf, m, 0), b_half(buf, m, 1)); }
 
@@ -472,7 +550,7 @@ struct ProductWg {
     __device__ __forceinline__ float token_scale(int s, int m) const
     {
         const uint32_t p = lds0 + S::kScales + (batch % kScaleRing) * S::kScaleBatch;
-        const uint32_t row = (uint32_t)((wm * MF + m) * 16 + (lane & 15));
+        const uint32_t row = (uint32_t)((m * S::WM + wm) * 16 + (lane & 15));
         // a row's four words side by side, four rows of words, or one word a row
         const uint32_t at = p + row * (a.s_row != 1 && !a.s_packed ? 16u : 4u) +
                             (uint32_t)(s & 3) * (a.s_packed ? 0u : a.s_row == 1 ? MT * 4u : 4u);
@@ -485,7 +563,7 @@ struct ProductWg {
     __device__ __forceinline__ float weight_scale(int s, int up) const
     {
         const uint8_t *p = lds + S::kScales + (batch % kScaleRing) * S::kScaleBatch + MT * 16;
-        const int block = EPI == kPlain ? wn * NF * 16 / 128 : up;
+        const int block = EPI == kPlain ? wn : up;
         return *reinterpret_cast<const float *>(p + block * 16 + (s & 3) * 4);
     }
 
@@ -505,106 +583,123 @@ struct ProductWg {
     }
 
     // fp8: the waiting sums of A fragment n into acc.
-    __device__ __forceinline__ void add_part(int n, int m)
+    template <int M>
+    static __device__ __forceinline__ void add_part(Work<M> &k, int n, int m)
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(part[m][i], part_s[m], acc[n][m][i]);
+        for (int i = 0; i < 4; ++i) k.acc[n][m][i] = fmaf(k.part[m][i], k.part_s[m], k.acc[n][m][i]);
         // here, not where the compiler would gather the additions of all fragments (whose sums then fill the registers)
-        asm volatile("" : "+v"(acc[n][m]));
+        asm volatile("" : "+v"(k.acc[n][m]));
     }
 
-    // Stage s of the tile, in LDS buffer buf, its first fragments in registers;
-    // leaves the next stage's there and loads a stage into buf.
+    // Stage s of the tile, in the buffers buf_a and buf_b, its first fragments in
+    // registers; leaves the next stage's there and loads into the buffers.
     //
     // The order is fixed by hand: every matrix instruction is followed by a
-    // share of the other work.  The barrier stands where the last A fragments of
-    // the stage are in registers; behind it the buffer is free for the loads of
-    // stage s + kBufs, and the next stage's fragments are read.  fp8: the sums
-    // of a stage are scaled and added while the next fragment's are under way.
-    template <bool BUSY, typename F>
-    __device__ __forceinline__ void run_stage(int buf, int s, F &&next)
+    // share of the other work.  B's fragments are in registers from the stage's
+    // beginning on: behind the first barrier B's buffer takes a later stage.  The
+    // second barrier stands where the last A fragments are in registers, and the
+    // next stage has arrived: behind it A's buffer takes a later stage, and the
+    // next stage's fragments are read.  (All loads behind the second barrier:
+    // 131072 rows of 128 experts, K = N = 4096, bf16, 4.02 ms.)  fp8: the sums of a
+    // stage are scaled and added while the next fragment's are under way.
+    template <int M>
+    __device__ __forceinline__ void run_stage(Work<(M > 0 ? M : 1)> &k, int s)
     {
-        const int nbuf = buf + 1 == S::kBufs ? 0 : buf + 1;
-        constexpr int kLeft = (S::kBufs - 2) * S::kUnits;
-        if constexpr (!BUSY) {
-            sync_stage<kLeft>();
-            load_next(buf, next);
+        const int next_a = buf_a + 1 == S::kABufs ? 0 : buf_a + 1, next_b = buf_b + 1 == S::kBBufs ? 0 : buf_b + 1;
+        if constexpr (M == 0) {
+            __builtin_amdgcn_s_barrier();
+            load_all_b(buf_b);
+            sync_stage<S::kLeft>();
+            load_all_a(buf_a);
         } else {
-            float sc[MF], sc2[MF];
+            float sc[M], sc2[M];
             if constexpr (FP8) {
                 const bool real = (int64_t)s * kLine < a.K;  // a stage past the row's end has no scales
                 const float g = weight_scale(s, 0), u = EPI == kPlain ? 0.0f : weight_scale(s, 1);
 #pragma unroll
-                for (int m = 0; m < MF; ++m) {
+                for (int m = 0; m < M; ++m) {
                     const float t = token_scale(s, m);
                     sc[m] = real ? t * g : 0.0f;
                     sc2[m] = real && EPI != kPlain ? t * u : 0.0f;
                 }
             }
             Units u;
-            constexpr int kPer = FP8 ? MF : 2 * MF, kAfter = D * kPer;       // matrix instructions per fragment, after the barrier
+            // matrix instructions per fragment, between the barriers, after them
+            constexpr int kPer = FP8 ? M : 2 * M, kBetween = (NF - D - 1) * kPer, kAfter = D * kPer;
+            static_assert(NF - D > 1, "steps between the barriers");
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
-                if (n == NF - D) {
-                    sync_stage<kLeft>();
-                    u = begin_load(buf, next);
+                if (n == 1) {
+                    begin_b(u, buf_b);
+                    __builtin_amdgcn_s_barrier();
                 }
-                fa[(n + D) % R] = a_fragment(n + D < NF ? buf : nbuf, (n + D) % NF);
+                if (n == NF - D) {
+                    begin_a(u, buf_a);
+                    sync_stage<S::kLeft>();
+                }
+                k.fa[(n + D) % R] = a_fragment(n + D < NF ? buf_a : next_a, (n + D) % NF);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int x = 0; x < kPer; ++x) {
-                    const int m = x % MF;
+                    const int m = x % M;
                     if constexpr (FP8) {
-                        add_part((n + NF - 1) % NF, m);
-                        part[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[n % R], fb[m], f32x4{}, 0, 0, 0, 0, 0, 0);
-                        part_s[m] = EPI != kPlain && n >= NF / 2 ? sc2[m] : sc[m];
+                        add_part(k, (n + NF - 1) % NF, m);
+                        k.part[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k.fa[n % R], k.fb[m], f32x4{}, 0, 0, 0, 0, 0, 0);
+                        k.part_s[m] = EPI != kPlain && n >= NF / 2 ? sc2[m] : sc[m];
                     } else {
-                        acc[n][m] = mma(fa[n % R], fb[m], acc[n][m], x / MF);
+                        k.acc[n][m] = mma(k.fa[n % R], k.fb[m], k.acc[n][m], x / M);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                     // B's registers take the next stage's as soon as they are used up
                     if (n == NF - 1) {
                         if constexpr (FP8)
-                            fb[m] = b_fragment(nbuf, m);
+                            k.fb[m] = b_fragment(next_b, m);
                         else
-                            fb[m] = x < MF ? join(b_half(nbuf, m, 0), half_of(fb[m], 1)) : join(half_of(fb[m], 0), b_half(nbuf, m, 1));
+                            k.fb[m] = x < M ? join(b_half(next_b, m, 0), half_of(k.fb[m], 1)) : join(half_of(k.fb[m], 0), b_half(next_b, m, 1));
                     }
-                    if (n >= NF - D) share((n - (NF - D)) * kPer + x, kAfter, S::kUnits, [&](int j) { load_unit(u, j); });
+                    if (n >= 1 && n < NF - D) share((n - 1) * kPer + x, kBetween, S::kBUnits, [&](int j) { load_b(u, j); });
+                    if (n >= NF - D) share((n - (NF - D)) * kPer + x, kAfter, S::kAUnits, [&](int j) { load_a(u, j); });
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
     }
 
-    // A tile's products into acc; returns the buffer of the next tile's first
-    // stage.
-    template <bool BUSY, typename F>
-    __device__ __forceinline__ int run_tile(int buf, F &&next)
+    // A tile's products into acc, M fragments of B a wave (none: only its share of
+    // the loads).
+    template <int M>
+    __device__ __forceinline__ void run_tile()
     {
-        if constexpr (BUSY) {
+        Work<(M > 0 ? M : 1)> k;
+        if constexpr (M > 0) {
 #pragma unroll
             for (int i = 0; i < NF; ++i)
 #pragma unroll
-                for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{};
+                for (int j = 0; j < M; ++j) k.acc[i][j] = f32x4{};
 #pragma unroll
-            for (int j = 0; j < D; ++j) fa[j] = a_fragment(buf, j);
+            for (int j = 0; j < D; ++j) k.fa[j] = a_fragment(buf_a, j);
 #pragma unroll
-            for (int j = 0; j < MF; ++j) {
-                fb[j] = b_fragment(buf, j);
-                part[j] = f32x4{};
-                part_s[j] = 0.0f;
+            for (int j = 0; j < M; ++j) {
+                k.fb[j] = b_fragment(buf_b, j);
+                k.part[j] = f32x4{};
+                k.part_s[j] = 0.0f;
             }
         }
-        for (int s = 0; s < stages; ++s) {
-            run_stage<BUSY>(buf, s, next);
-            if (FP8 && ((s & 3) == 3 || s == stages - 1)) ++batch;
-            buf = buf + 1 == S::kBufs ? 0 : buf + 1;
+        for (int s = 0; s < at.stages; ++s) {
+            run_stage<M>(k, s);
+            if (FP8 && ((s & 3) == 3 || s == at.stages - 1)) ++batch;
+            buf_a = buf_a + 1 == S::kABufs ? 0 : buf_a + 1;
+            buf_b = buf_b + 1 == S::kBBufs ? 0 : buf_b + 1;
         }
-        if constexpr (BUSY && FP8) {
+        if constexpr (M > 0 && FP8) {
 #pragma unroll
-            for (int m = 0; m < MF; ++m) add_part(NF - 1, m);
+            for (int m = 0; m < M; ++m) add_part(k, NF - 1, m);
         }
-        return buf;
+        if constexpr (FP8 && EPI == kSwiglu)
+            store_tile_fp8<M>(k);
+        else if constexpr (M > 0)
+            store_tile(k);
     }
 
     // ---- results ----
@@ -657,7 +752,8 @@ struct ProductWg {
         }
     }
 
-    __device__ __forceinline__ void store_tile() const
+    template <int M>
+    __device__ __forceinline__ void store_tile(const Work<M> &k) const
     {
         const int64_t ld = FORM == kFwd ? (EPI == kSwiglu ? a.N / 2 : a.N) : a.K;
         const bool vector = ld % 8 == 0 && (EPI != kSwigluGrad || a.N / 2 % 8 == 0) && ((uintptr_t)a.out & 15) == 0;
@@ -665,10 +761,10 @@ struct ProductWg {
         constexpr int H = EPI == kPlain ? NF : NF / 2;       // blocks of output columns
         constexpr int NB = H < 4 ? H : 4;
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int t = (wm * MF + m) * 16 + (lane & 15);
-            const bool live = t < live_m;
-            uint16_t *row = a.out + (FORM == kDw ? (int64_t)e * a.N + row0 + t : row0 + t) * ld + n0;
+        for (int m = 0; m < M; ++m) {
+            const int t = (m * S::WM + wm) * 16 + (lane & 15);
+            const bool live = t < at.live_m;
+            uint16_t *row = a.out + (FORM == kDw ? (int64_t)at.e * a.N + at.row0 + t : at.row0 + t) * ld + at.n0;
 #pragma unroll
             for (int q = 0; q < H / NB; ++q) {
                 const int c = (wn * H + q * NB) * 16;
@@ -676,22 +772,22 @@ struct ProductWg {
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     if constexpr (EPI == kPlain) {
-                        v[j] = acc[q * NB + j][m];
+                        v[j] = k.acc[q * NB + j][m];
                     } else {
-                        const f32x4 gate = acc[q * NB + j][m], up = acc[H + q * NB + j][m];
+                        const f32x4 gate = k.acc[q * NB + j][m], up = k.acc[H + q * NB + j][m];
                         f32x4 d = {};
                         if constexpr (EPI == kSwigluGrad) {
-                            const int at = c + 16 * j + 4 * (lane >> 4);
-                            const uint16_t *p = a.dh + (row0 + t) * I + n0 + at;
+                            const int col = c + 16 * j + 4 * (lane >> 4);
+                            const uint16_t *p = a.dh + (at.row0 + t) * I + at.n0 + col;
                             if (live && ((I & 3) == 0 && ((uintptr_t)a.dh & 7) == 0)) {
-                                if (at < live_n) {
+                                if (col < at.live_n) {
                                     const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
                                     d = f32x4{bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
                                 }
                             } else if (live) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    if (at + i < live_n) d[i] = __uint_as_float((uint32_t)p[i] << 16);
+                                    if (col + i < at.live_n) d[i] = __uint_as_float((uint32_t)p[i] << 16);
                             }
                         }
 #pragma unroll
@@ -706,8 +802,8 @@ struct ProductWg {
                         }
                     }
                 }
-                store_blocks<NB>(v, row + c, live_n - c, live, vector);
-                if constexpr (EPI == kSwigluGrad) store_blocks<NB>(w, row + I + c, live_n - c, live, vector);
+                store_blocks<NB>(v, row + c, at.live_n - c, live, vector);
+                if constexpr (EPI == kSwigluGrad) store_blocks<NB>(w, row + I + c, at.live_n - c, live, vector);
                 __builtin_amdgcn_sched_barrier(0);           // one group's temporaries at a time
             }
         }
@@ -715,21 +811,22 @@ struct ProductWg {
 
     // SwiGLU values in fp8: a tile's 128 columns are one group, so the waves
     // of a row exchange their largest magnitudes.  Every wave comes here.
-    __device__ __forceinline__ void store_tile_fp8(bool busy)
+    template <int M>
+    __device__ __forceinline__ void store_tile_fp8(Work<(M > 0 ? M : 1)> &k)
     {
         constexpr int H = NF / 2;
         float *amax = reinterpret_cast<float *>(lds + S::kAmax);
-        if (busy) {
+        if constexpr (M > 0) {
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
+            for (int m = 0; m < M; ++m) {
                 uint32_t top = 0;                            // magnitudes as integers, NaNs left out
 #pragma unroll
                 for (int j = 0; j < H; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float g = acc[j][m][i];
-                        const float h = g / (1.0f + __expf(-g)) * acc[H + j][m][i];
-                        acc[j][m][i] = h;
+                        const float g = k.acc[j][m][i];
+                        const float h = g / (1.0f + __expf(-g)) * k.acc[H + j][m][i];
+                        k.acc[j][m][i] = h;
                         const uint32_t u = __float_as_uint(h) & 0x7FFFFFFFu;
                         top = u <= 0x7F800000u && u > top ? u : top;
                     }
@@ -739,27 +836,27 @@ struct ProductWg {
                 o = top;
                 swap_rows16(top, o);
                 top = top > o ? top : o;
-                if (lane < 16) amax[wn * MT + (wm * MF + m) * 16 + lane] = __uint_as_float(top);
+                if (lane < 16) amax[wn * MT + (m * S::WM + wm) * 16 + lane] = __uint_as_float(top);
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (!busy) return;
+        if constexpr (M == 0) return;
         const int64_t I = a.N / 2;
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int t = (wm * MF + m) * 16 + (lane & 15);
+        for (int m = 0; m < M; ++m) {
+            const int t = (m * S::WM + wm) * 16 + (lane & 15);
             float am = amax[t];
 #pragma unroll
             for (int x = 1; x < S::WN; ++x) am = fmaxf(am, amax[x * MT + t]);
             const Fp8Group q(am, (a.s_flags & CDL_FP8_SCALE_UE8M0) != 0);
-            const bool live = t < live_m;
-            const int64_t row = row0 + t;
+            const bool live = t < at.live_m;
+            const int64_t row = at.row0 + t;
             uint32_t w[H];
 #pragma unroll
-            for (int j = 0; j < H; ++j) w[j] = q.code4(acc[j][m][0], acc[j][m][1], acc[j][m][2], acc[j][m][3]);
-            uint8_t *to = a.hq + row * I + n0 + wn * H * 16;
+            for (int j = 0; j < H; ++j) w[j] = q.code4(k.acc[j][m][0], k.acc[j][m][1], k.acc[j][m][2], k.acc[j][m][3]);
+            uint8_t *to = a.hq + row * I + at.n0 + wn * H * 16;
             const int g = lane >> 4;
             if constexpr (H == 4) {
                 swap_halves(w[0], w[2]);
@@ -773,8 +870,8 @@ struct ProductWg {
                     if (live) *reinterpret_cast<uint32_t *>(to + 16 * j + 4 * g) = w[j];
             }
             if (live && lane < 16 && wn == 0) {
-                const int64_t grp = n0 / 128;
-                const int64_t r = a.h_mat ? e * a.h_mat + (row0 - (int64_t)e * a.cap + t) * a.h_row : row * a.h_row;
+                const int64_t grp = at.n0 / 128;
+                const int64_t r = a.h_mat ? at.e * a.h_mat + (at.m0 + t) * a.h_row : row * a.h_row;
                 if (a.s_packed) {
                     uint8_t *word = static_cast<uint8_t *>(a.hs) + (r + grp / 4 * a.h_group) * 4;
                     word[grp % 4] = q.exponent();
@@ -786,21 +883,6 @@ struct ProductWg {
         }
     }
 };
-
-// Tiles of the weights' gradient: the tile ids run over the experts, each with
-// tiles_m x tiles_n of them, whatever its count.
-__device__ __forceinline__ GroupedTile dw_tile(const ProductArgs &a, int tiles_m, int tiles_n, int64_t id)
-{
-    GroupedTile t;
-    const int64_t per = (int64_t)tiles_m * tiles_n;
-    t.e = __builtin_amdgcn_readfirstlane((int)(id / per));
-    const int local = (int)(id - t.e * per);
-    t.n = __builtin_amdgcn_readfirstlane(local / tiles_m);
-    t.m = __builtin_amdgcn_readfirstlane(local % tiles_m);
-    bool bad;
-    t.count = grouped_rows(a, t.e, &t.begin, &bad);
-    return t;
-}
 
 template <bool FP8, ProductForm FORM, ProductEpilogue EPI, int MT>
 __global__ __launch_bounds__(kProductThreads) void product_kernel(ProductArgs a, int tiles_m, int tiles_n)
@@ -816,31 +898,25 @@ __global__ __launch_bounds__(kProductThreads) void product_kernel(ProductArgs a,
     const int32_t per = (total + 7) / 8, step = (int32_t)(gridDim.x / 8);
     const int32_t first = (int32_t)(blockIdx.x & 7) * per;
     const int32_t last = first + per < total ? first + per : total;
-    int32_t id = first + (int32_t)(blockIdx.x >> 3);         // the tile being loaded
+    int32_t id = first + (int32_t)(blockIdx.x >> 3);
     if (id >= last) return;
     __syncthreads();
-    Wg w(a, lds);
-    auto tile = [&] { return FORM == kDw ? dw_tile(a, tiles_m, tiles_n, id) : grouped_tile(a, ends, tiles_n, id); };
-    auto next = [&] {
-        id += step;
-        if (id < last)
-            w.set_tile(tile());
+    Wg w(a, lds, ends, tiles_m, tiles_n, last, step);
+    w.start(id);
+    for (; id < last; id += step) {
+        w.at = w.at_b;                                       // (B is not yet past this tile)
+        const bool busy = w.wm * 16 < w.at.live_m;           // the wave has a live row
+        const int blocks = busy ? (w.at.live_m + 63) / 64 : 0;
+        if (FORM == kDw || blocks == S::MF)                  // (gradients of the weights: all but a last tile are full)
+            w.template run_tile<S::MF>();
+        else if (blocks == 0)
+            w.template run_tile<0>();
+        else if (blocks == 1)
+            w.template run_tile<1>();
+        else if (blocks == 2 || S::MF < 4)
+            w.template run_tile<(S::MF > 2 ? 2 : 1)>();
         else
-            w.set_no_tile();
-    };
-    w.set_tile(tile());
-    w.load_stage = 0;
-    for (int b = 0; b < S::kBufs; ++b) w.load_next(b, next);
-    sync_stage<(S::kBufs - 1) * S::kUnits>();
-    int buf = 0;
-    for (int32_t at = id; at < last; at += step) {
-        w.take_tile();
-        const bool busy = w.wm * S::MF * 16 < w.live_m;      // the wave has a live row
-        buf = busy ? w.template run_tile<true>(buf, next) : w.template run_tile<false>(buf, next);
-        if constexpr (FP8 && EPI == kSwiglu)
-            w.store_tile_fp8(busy);
-        else if (busy)
-            w.store_tile();
+            w.template run_tile<(S::MF > 3 ? 3 : 1)>();
     }
     // nothing may be on its way to this workgroup's LDS when it ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -885,6 +961,39 @@ int launch_product_tiles(const ProductArgs &a, hipStream_t stream)
     return launch_status();
 }
 
+// Rows of a tile, 128, 192 or 256: the fewest rounds of the workgroups, weighed
+// by what a round costs (1.03, 1.33 and 1.59 us a stage where the matrix
+// instructions bound it).  The host sees the rows of the whole buffer only: an
+// expert is taken to have their average, in one tile where that fills four
+// fifths of it, otherwise half a tile more; a second round counts whole.  Measured, us for 128 / 192 / 256
+// rows, bf16, 32 experts, K = 7168, N = 4096: 94 rows an expert 338 / 339 / 362,
+// 128 rows 403 / 354 / 373, 172 rows 515 / 430 / 395, 256 rows 623 / 603 / 559,
+// 512 rows 1042 / 942 / 892; 4 experts of 512 rows, K = N = 4096: 121 / 85 / 99;
+// one of 4096 rows: 138 / 159 / 112; 8 of 250 rows, K = N = 1024: 21 / 26 / 30.
+// Padded buffers are mostly empty in decode, where the weights' bytes count
+// and three stages of them in LDS pay: 4 rows an expert, 32 experts, K = 7168,
+// N = 4096, bf16 307 / 307 / 328, fp8 162 / 161 / 175.
+template <ProductForm FORM, ProductEpilogue EPI>
+int product_tile_rows(const ProductArgs &a)
+{
+    if (!a.seg) return 192;
+    const int64_t width = FORM == kDx ? a.K : EPI == kPlain ? a.N : a.N / 2, cols = EPI == kPlain ? kProductNT : kProductNT / 2;
+    const double tiles_n = (double)((width + cols - 1) / cols), r = (double)a.rows / a.L;
+    int best = 0;
+    double least = 0;
+    for (int mt = 128; mt <= 256; mt += 64) {
+        double tm = a.L == 1 ? (double)((a.rows + mt - 1) / mt) : r <= 0.8 * mt ? 1.0 : r / mt + 0.5;
+        const double tiles = tm * a.L * tiles_n, rounds = tiles <= kProductWgs ? 1.0 : tiles / kProductWgs;
+        const double whole = rounds <= 1.0 ? 1.0 : rounds <= 2.0 ? 2.0 : rounds;
+        const double cost = whole * (mt == 128 ? 1.03 : mt == 192 ? 1.33 : 1.59);
+        if (best == 0 || cost < least) {
+            best = mt;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 template <bool FP8, ProductForm FORM, ProductEpilogue EPI>
 int launch_product(const ProductArgs &a, hipStream_t stream)
 {
@@ -893,9 +1002,10 @@ int launch_product(const ProductArgs &a, hipStream_t stream)
     } else {
         // (an empty buffer: only the check of the counts is left)
         if (a.rows == 0 && !a.status) return CDL_OK;
-        const int64_t small_tiles = (a.rows / 64 + a.L / 2) * ((a.N + kProductNT - 1) / kProductNT);
-        const bool large = a.seg ? a.rows / a.L >= 64 && small_tiles > kProductWgs : a.cap > 256;
-        return large ? launch_product_tiles<FP8, FORM, EPI, 256>(a, stream) : launch_product_tiles<FP8, FORM, EPI, 64>(a, stream);
+        const int mt = product_tile_rows<FORM, EPI>(a);
+        return mt == 256   ? launch_product_tiles<FP8, FORM, EPI, 256>(a, stream)
+               : mt == 192 ? launch_product_tiles<FP8, FORM, EPI, 192>(a, stream)
+                           : launch_product_tiles<FP8, FORM, EPI, 128>(a, stream);
     }
 }
 
