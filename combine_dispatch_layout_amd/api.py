@@ -1043,21 +1043,30 @@ def moe_layer_mxfp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch
 # products grouped by expert in bf16 and fp8
 # ---------------------------------------------------------------------------
 
+def _have(t, name: str, dtype, shape, dev) -> None:
+    """_need and _same_device in one: the calls below have many operands and
+    little to do, so what they usually get is seen in one expression."""
+    if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        _same_device(dev, **{name: t})
+
+
 def _groups(rows: torch.Tensor, name: str, L: int, counts, seg_indptr, status):
     """Checked rows of the grouped products, [rows, n] with seg_indptr and
     [L, cap, n] without: (number of rows, cap)."""
-    _need(counts, "counts", torch.int32, (L,))
-    if seg_indptr is not None:
-        _need(seg_indptr, "seg_indptr", torch.int64, (L + 1,))
-        if rows.dim() != 2:
-            raise ValueError("%s must be [rows, n] with seg_indptr, got %s" % (name, tuple(rows.shape)))
-    elif rows.dim() != 3 or rows.shape[0] != L:
-        raise ValueError("%s must be [L, cap, n] with L = %d without seg_indptr, got %s" % (name, L, tuple(rows.shape)))
+    dev = rows.device
+    _have(counts, "counts", torch.int32, (L,), dev)
     if status is not None:
         _need(status, "status", torch.int32)
-    _same_device(rows.device, counts=counts, seg_indptr=seg_indptr, status=status)
-    cap = 0 if seg_indptr is not None else rows.shape[1]
-    return (rows.shape[0] if seg_indptr is not None else L * cap), cap
+        _same_device(dev, status=status)
+    if seg_indptr is not None:
+        _have(seg_indptr, "seg_indptr", torch.int64, (L + 1,), dev)
+        if rows.dim() != 2:
+            raise ValueError("%s must be [rows, n] with seg_indptr, got %s" % (name, tuple(rows.shape)))
+        return rows.shape[0], 0
+    if rows.dim() != 3 or rows.shape[0] != L:
+        raise ValueError("%s must be [L, cap, n] with L = %d without seg_indptr, got %s" % (name, L, tuple(rows.shape)))
+    return L * rows.shape[1], rows.shape[1]
 
 
 def _bf16_weights(w: torch.Tensor, name: str) -> Tuple[int, int, int]:
@@ -1069,9 +1078,10 @@ def _bf16_weights(w: torch.Tensor, name: str) -> Tuple[int, int, int]:
 
 def _product_rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, width: int) -> torch.Tensor:
     """bf16 rows [*like's rows, width] on its device: the given tensor, checked, or a new one."""
+    shape = (*like.shape[:-1], width)
     if t is None:
-        return torch.empty(*like.shape[:-1], width, dtype=torch.bfloat16, device=like.device)
-    _need(t, name, torch.bfloat16, (*like.shape[:-1], width))
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    _have(t, name, torch.bfloat16, shape, like.device)
     return t
 
 
@@ -1084,10 +1094,10 @@ def _bf16_product(what, x, w, counts, seg_indptr, out, status, width_of, extra=N
     n, width = width_of(N)
     more = ()
     if extra is not None:
-        _need(extra, "dh", torch.bfloat16, (*x.shape[:-1], n))
+        _have(extra, "dh", torch.bfloat16, (*x.shape[:-1], n), x.device)
         more = (_ptr(extra),)
     out = _product_rows(out, "out", x, width)
-    _same_device(x.device, w=w, out=out, dh=extra)
+    _same_device(x.device, w=w)
     _launch(what, x.device, _ptr(x), rows, K, _ptr(w), L, n, *more, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out),
             _ptr(status))
     return out
@@ -1141,7 +1151,7 @@ def grouped_bf16_dx(dy: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg
         raise ValueError("dy must have rows of N = %d elements, got %s" % (N, tuple(dy.shape)))
     rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
     out = _product_rows(out, "out", dy, K)
-    _same_device(dy.device, w=w, out=out)
+    _same_device(dy.device, w=w)
     _launch("cdl_grouped_bf16_dx", dy.device, _ptr(dy), rows, N, _ptr(w), L, K, _ptr(counts), _ptr(seg_indptr), cap,
             _ptr(out), _ptr(status))
     return out
@@ -1161,8 +1171,8 @@ def grouped_bf16_dw(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, seg
     N, K = dy.shape[-1], x.shape[-1]
     if out is None:
         out = torch.empty(L, N, K, dtype=torch.bfloat16, device=dy.device)
-    _need(out, "out", torch.bfloat16, (L, N, K))
-    _same_device(dy.device, x=x, out=out)
+    _have(out, "out", torch.bfloat16, (L, N, K), dy.device)
+    _same_device(dy.device, x=x)
     _launch("cdl_grouped_bf16_dw", dy.device, _ptr(dy), _ptr(x), rows, N, K, L, _ptr(counts), _ptr(seg_indptr), cap,
             _ptr(out), _ptr(status))
     return out
@@ -1178,10 +1188,10 @@ def _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status)
         raise CdlError(-3, "fp8 product (K must be a multiple of %d)" % FP8_GROUP)
     if q.dim() < 2 or q.shape[-1] != K:
         raise ValueError("q must have rows of K = %d bytes, got %s" % (K, tuple(q.shape)))
-    _need(w_scales, "w_scales", torch.float32, (L, -(-N // FP8_GROUP), K // FP8_GROUP))
+    _have(w_scales, "w_scales", torch.float32, (L, -(-N // FP8_GROUP), K // FP8_GROUP), q.device)
     rows, cap = _groups(q, "q", L, counts, seg_indptr, status)
     _check_scale_buffer(scales, rows, K, scale_flags, cap if seg_indptr is None else rows)
-    _same_device(q.device, scales=scales, w_q=w_q, w_scales=w_scales)
+    _same_device(q.device, scales=scales, w_q=w_q)
     return L, N, K, rows, cap
 
 
@@ -1194,7 +1204,6 @@ def grouped_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scal
     as quant_fp8_blocks does.  Rows and counts as for grouped_bf16."""
     L, N, K, rows, cap = _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status)
     out = _product_rows(out, "out", q, N)
-    _same_device(q.device, out=out)
     _launch("cdl_grouped_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, K, _ptr(w_q), _ptr(w_scales), L, N,
             _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status))
     return out
@@ -1275,7 +1284,7 @@ def dequant_fp8(q: torch.Tensor, scales: torch.Tensor, scale_flags: int = 0,
     rpm = q.shape[-2]
     _check_scale_buffer(scales, rows, H, scale_flags, rpm)
     out = _product_rows(out, "out", q, H)
-    _same_device(q.device, scales=scales, out=out)
+    _same_device(q.device, scales=scales)
     _launch("cdl_dequant_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, H, rpm, _ptr(out))
     return out
 
@@ -1284,21 +1293,33 @@ def dequant_fp8(q: torch.Tensor, scales: torch.Tensor, scale_flags: int = 0,
 # root-mean-square norm
 # ---------------------------------------------------------------------------
 
-def _norm_args(x, weight, eps, **others):
+def _norm_args(x, weight, eps) -> Tuple[int, int]:
     """Checked bf16 rows x [..., H] and weight [H]: (T, H)."""
     _need(x, "x", torch.bfloat16)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., H]")
     H = x.shape[-1]
-    _need(weight, "weight", torch.bfloat16, (H,))
+    _have(weight, "weight", torch.bfloat16, (H,), x.device)
     if not eps >= 0:
         raise ValueError("eps must be >= 0, got %r" % (eps,))
-    _same_device(x.device, weight=weight, **others)
     return x.numel() // H, H
 
 
+def _norm_residual(x, residual, residual_out):
+    """The checked residual_out, new where there is none; None without residual."""
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs residual")
+        return None
+    _have(residual, "residual", torch.bfloat16, x.shape, x.device)
+    return _same_rows(residual_out, "residual_out", x)
+
+
 def _same_rows(t: Optional[torch.Tensor], name: str, x: torch.Tensor) -> torch.Tensor:
-    return _product_rows(t, name, x, x.shape[-1])
+    if t is None:
+        return torch.empty_like(x)
+    _have(t, name, torch.bfloat16, x.shape, x.device)
+    return t
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -1308,12 +1329,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     x + residual rounded to bf16 (what the residual path keeps is what is
     normed); then returns (out, h), otherwise out.  out and residual_out may be
     x or residual itself."""
-    T, H = _norm_args(x, weight, eps, residual=residual, out=out, residual_out=residual_out)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out needs residual")
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, x.shape)
-        residual_out = _same_rows(residual_out, "residual_out", x)
+    T, H = _norm_args(x, weight, eps)
+    residual_out = _norm_residual(x, residual, residual_out)
     out = _same_rows(out, "out", x)
     _launch("cdl_rms_norm", x.device, _ptr(x), _ptr(residual), _ptr(weight), float(eps), T, H, _ptr(out),
             _ptr(residual_out))
@@ -1327,25 +1344,23 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     128 as the fp8 dispatch quantises rows (amax / 448, or the formats of
     scale_flags).  Returns (q [T, H] uint8, scales) and with residual also h;
     `out`, where given, receives the bf16 rows as well (a router's input)."""
-    T, H = _norm_args(x, weight, eps, residual=residual, out=out, residual_out=residual_out)
+    T, H = _norm_args(x, weight, eps)
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
     if H % FP8_GROUP:
         raise CdlError(-3, "rms_norm_fp8 (H must be a multiple of %d)" % FP8_GROUP)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out needs residual")
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, x.shape)
-        residual_out = _same_rows(residual_out, "residual_out", x)
+    residual_out = _norm_residual(x, residual, residual_out)
     if out is not None:
         out = _same_rows(out, "out", x)
     if out_q is None:
-        out_q = torch.empty(T, H, dtype=torch.uint8, device=x.device)
-    _need(out_q, "out_q", torch.uint8, (T, H))
+        out_q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+    else:
+        _have(out_q, "out_q", torch.uint8, (T, H), x.device)
     if out_scales is None:
         out_scales = new_scale_tensor(T, H, scale_flags, x.device)
-    _check_scale_buffer(out_scales, T, H, scale_flags, T)
-    _same_device(x.device, out_q=out_q, out_scales=out_scales)
+    else:
+        _check_scale_buffer(out_scales, T, H, scale_flags, T)
+        _same_device(x.device, out_scales=out_scales)
     _launch("cdl_rms_norm_fp8", x.device, _ptr(x), _ptr(residual), _ptr(weight), float(eps), T, H, _ptr(out_q),
             _ptr(out_scales), int(scale_flags), _ptr(out), _ptr(residual_out))
     return (out_q, out_scales) if residual is None else (out_q, out_scales, residual_out)
@@ -1366,20 +1381,23 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
     the gradient of h, so of x and of residual alike; dresidual, the gradient
     that reaches h past the norm, is added to it before the one rounding.  out
     may be dy, h or dresidual itself.  Deterministic."""
-    T, H = _norm_args(h, weight, eps, dy=dy, dresidual=dresidual, out=out, dweight=dweight, workspace=workspace)
-    _need(dy, "dy", torch.bfloat16, h.shape)
+    T, H = _norm_args(h, weight, eps)
+    _have(dy, "dy", torch.bfloat16, h.shape, h.device)
     if dresidual is not None:
-        _need(dresidual, "dresidual", torch.bfloat16, h.shape)
+        _have(dresidual, "dresidual", torch.bfloat16, h.shape, h.device)
     out = _same_rows(out, "out", h)
     if dweight is None:
         dweight = torch.empty(H, dtype=torch.float32, device=h.device)
-    _need(dweight, "dweight", torch.float32, (H,))
+    else:
+        _have(dweight, "dweight", torch.float32, (H,), h.device)
     need = rms_norm_grad_workspace_size(T, H)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
-    _need_gpu(workspace, "workspace")
-    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
-        raise ValueError("workspace too small: need %d bytes" % need)
+    else:
+        _need_gpu(workspace, "workspace")
+        if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+            raise ValueError("workspace too small: need %d bytes" % need)
+        _same_device(h.device, workspace=workspace)
     _launch("cdl_rms_norm_grad", h.device, _ptr(dy), _ptr(h), _ptr(weight), _ptr(dresidual), float(eps), T, H, _ptr(out),
             _ptr(dweight), _ptr(workspace), workspace.numel() * workspace.element_size())
     return out, dweight

@@ -130,26 +130,11 @@ __device__ __forceinline__ void store_scale(const NormArgs &a, const Fp8Group &q
 }
 
 // 8 values of a row's group (16 lanes) to codes.
-__device__ __forceinline__ u32x2 quant8(const float (&y)[8], const Fp8Group &q, float amax)
+__device__ __forceinline__ u32x2 quant8(const float (&y)[8], const Fp8Group &q)
 {
-    // the quotient by one reciprocal with a correction step, as the dispatch's
-    // (3 instructions an element against the division's 10); tiny and
-    // non-finite groups divide
-    if (q.ue8m0 || __ballot(!(amax >= 0x1p-96f && amax < __builtin_huge_valf())))
-        return u32x2{q.code4(y[0], y[1], y[2], y[3]), q.code4(y[4], y[5], y[6], y[7])};
-    const float r0 = __builtin_amdgcn_rcpf(q.scale);
-    const float r = fmaf(fmaf(-q.scale, r0, 1.0f), r0, r0);
-    float c[8];
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q0 = y[i] * r;
-        const float d = fmaf(-fmaf(q0, q.scale, -y[i]), r, q0);
-        nan |= d != d;
-        c[i] = fminf(fmaxf(d, -448.0f), 448.0f);
-    }
-    if (nan) return u32x2{q.code4(y[0], y[1], y[2], y[3]), q.code4(y[4], y[5], y[6], y[7])};
-    return u32x2{pack4_e4m3(c[0], c[1], c[2], c[3]), pack4_e4m3(c[4], c[5], c[6], c[7])};
+    uint32_t c[2];
+    q.codes<2>(y, c);
+    return u32x2{c[0], c[1]};
 }
 
 template <int VEC, int NU, bool WAVE, bool FP8>
@@ -216,7 +201,7 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_kernel(NormArgs a)
                 m = dpp_umax_step<0x140>(half_row_umax(m));      // row_mirror: the other 8 of the group's 16 lanes
                 const float amax = __uint_as_float(m);
                 const Fp8Group q(amax, (a.flags & CDL_FP8_SCALE_UE8M0) != 0);
-                const u32x2 code = quant8(y, q, amax);
+                const u32x2 code = quant8(y, q);
                 store_scale(a, q, t, c / 128, (int64_t)((tid & ~(kWave - 1)) + j * P) * VEC / 128, c < H);
                 if (c < H) *reinterpret_cast<u32x2 *>(a.q + row + c) = code;
             }
@@ -282,7 +267,7 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_long_kernel(NormArgs a)
                 m = dpp_umax_step<0x140>(half_row_umax(m));
                 const float amax = __uint_as_float(m);
                 const Fp8Group q(amax, (a.flags & CDL_FP8_SCALE_UE8M0) != 0);
-                const u32x2 code = quant8(y, q, amax);
+                const u32x2 code = quant8(y, q);
                 store_scale(a, q, t, c / 128, first / 128, c < H);
                 if (c < H) *reinterpret_cast<u32x2 *>(a.q + row + c) = code;
             }
@@ -457,23 +442,26 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_grad_columns_kernel(Nor
     for (int i = 0; i < VEC; ++i) a.partial[(int64_t)blockIdx.y * a.H + c + i] = acc[i];
 }
 
-// dweight from the G partial sums: 64 columns a workgroup, the sums of 16
-// slices of G by 16 waves, then those in order.
+// dweight from the G partial sums: 32 columns a workgroup, 32 slices of G
+// summed side by side (8 loads under way each), then those in order.
+constexpr int kDwColumns = 32, kDwSlices = 32;
 __global__ __launch_bounds__(1024) void rms_norm_dweight_kernel(const float *__restrict__ partial, int G, int64_t H,
                                                                 float *__restrict__ dweight)
 {
-    __shared__ float lds[16][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t c = (int64_t)blockIdx.x * kWave + lane;
+    __shared__ float lds[kDwSlices][kDwColumns];
+    const int col = threadIdx.x % kDwColumns, slice = threadIdx.x / kDwColumns;
+    const int64_t c = (int64_t)blockIdx.x * kDwColumns + col;
     float s = 0.0f;
-    if (c < H)
-        for (int b = wave; b < G; b += 16) s += partial[(int64_t)b * H + c];
-    lds[wave][lane] = s;
+    if (c < H) {
+#pragma unroll 8
+        for (int b = slice; b < G; b += kDwSlices) s += partial[(int64_t)b * H + c];
+    }
+    lds[slice][col] = s;
     __syncthreads();
-    if (wave == 0 && c < H) {
+    if (slice == 0 && c < H) {
         float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v += lds[i][lane];
+        for (int i = 0; i < kDwSlices; ++i) v += lds[i][col];
         dweight[c] = v;
     }
 }
@@ -519,9 +507,8 @@ __global__ __launch_bounds__(256) void quant_fp8_blocks_kernel(const uint16_t *_
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (nb * 128 + r0 + 16 * i < N)
-                *reinterpret_cast<u32x2 *>(q + base + (r0 + 16 * i) * K) =
-                    u32x2{f.code4(u[i].at(0), u[i].at(1), u[i].at(2), u[i].at(3)),
-                          f.code4(u[i].at(4), u[i].at(5), u[i].at(6), u[i].at(7))};
+                *reinterpret_cast<u32x2 *>(q + base + (r0 + 16 * i) * K) = quant8(
+                    {u[i].at(0), u[i].at(1), u[i].at(2), u[i].at(3), u[i].at(4), u[i].at(5), u[i].at(6), u[i].at(7)}, f);
         __syncthreads();
     }
 }
@@ -626,7 +613,7 @@ int launch_norm_grad(const NormGradArgs &a, hipStream_t stream)
         int rc = launch_status();
         if (rc != CDL_OK) return rc;
     }
-    rms_norm_dweight_kernel<<<dim3((unsigned)((a.H + kWave - 1) / kWave)), dim3(1024), 0, stream>>>(a.partial, a.G, a.H, a.dweight);
+    rms_norm_dweight_kernel<<<dim3((unsigned)((a.H + kDwColumns - 1) / kDwColumns)), dim3(kDwColumns * kDwSlices), 0, stream>>>(a.partial, a.G, a.H, a.dweight);
     return launch_status();
 }
 

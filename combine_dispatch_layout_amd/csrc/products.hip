@@ -23,11 +23,11 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 // magnitude (over its values that are not NaN; infinite if one is): the
 // dispatch's quantisation, of 32-bit values.
 struct Fp8Group {
-    float scale;
+    float scale, inverse;
     int ex;                      // UE8M0: scale = 2^ex
-    bool ue8m0, empty;
+    bool ue8m0, empty, fast;
 
-    __device__ __forceinline__ Fp8Group(float amax, bool ue) : ex(-127), ue8m0(ue), empty(!(amax > 0.0f))
+    __device__ __forceinline__ Fp8Group(float amax, bool ue) : inverse(0.0f), ex(-127), ue8m0(ue), empty(!(amax > 0.0f)), fast(false)
     {
         if (ue8m0) {
             if (!empty) {
@@ -39,35 +39,57 @@ struct Fp8Group {
             scale = ldexpf(1.0f, ex);
         } else {
             scale = amax / 448.0f;                           // correctly rounded
+            // The quotient by one reciprocal with a correction step, as the
+            // dispatch's (3 instructions an element against the division's 10),
+            // where it cannot leave fp32's range.
+            // (one path for the whole wave)
+            fast = __ballot(!(amax >= 0x1p-96f && amax < __builtin_huge_valf())) == 0;
+            const float r = __builtin_amdgcn_rcpf(scale);
+            inverse = fmaf(fmaf(-scale, r, 1.0f), r, r);
         }
     }
     __device__ __forceinline__ uint8_t exponent() const { return (uint8_t)(ex + 127); }
-    __device__ __forceinline__ float quotient(float x) const
+    // 4 W values to W words of codes.  A NaN quotient (or an infinite one, of a
+    // power of two) takes the NaN code with x's sign.
+    template <int W>
+    __device__ __forceinline__ void codes(const float (&x)[4 * W], uint32_t (&out)[W]) const
     {
-        if (ue8m0) return ldexpf(x, -ex);
-        const float d = empty ? x : x / scale;               // correctly rounded
-        return d > 448.0f ? 448.0f : d < -448.0f ? -448.0f : d;
-    }
-    // a NaN quotient (or an infinite one, of a power of two) takes the NaN code with x's sign
-    __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) const
-    {
-        const float x[4] = {a, b, c, d};
-        float q[4];
-        bool odd = false;
+        float q[4 * W], sum = 0.0f;
+        // one branch a call, the same for the wave
+        if (fast) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[i] = quotient(x[i]);
-            odd |= !__builtin_isfinite(q[i]);
-        }
-        if (!odd) return pack4_e4m3(q[0], q[1], q[2], q[3]);
-        uint32_t r = 0;
+            for (int i = 0; i < 4 * W; ++i) {
+                // (up to 448 + 2^-15, which the conversion takes to 448)
+                const float t = x[i] * inverse;
+                q[i] = fmaf(-fmaf(t, scale, -x[i]), inverse, t);
+            }
+        } else if (ue8m0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool fin = __builtin_isfinite(q[i]);
-            const uint32_t code = fin ? pack2_e4m3(q[i], 0.0f) & 0xFFu : (__float_as_uint(x[i]) >> 24 & 0x80u) | 0x7Fu;
-            r |= code << (8 * i);
+            for (int i = 0; i < 4 * W; ++i) q[i] = ldexpf(x[i], -ex);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * W; ++i) {
+                const float d = empty ? x[i] : x[i] / scale; // correctly rounded
+                q[i] = d > 448.0f ? 448.0f : d < -448.0f ? -448.0f : d;
+            }
         }
-        return r;
+#pragma unroll
+        for (int i = 0; i < 4 * W; ++i) sum += q[i];
+#pragma unroll
+        for (int w = 0; w < W; ++w) out[w] = pack4_e4m3(q[4 * w], q[4 * w + 1], q[4 * w + 2], q[4 * w + 3]);
+        // (finite if every term is, |q| <= 464)
+        if (__builtin_expect(!__builtin_isfinite(sum), 0)) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                out[w] = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = q[4 * w + i];
+                    const uint32_t nan = (__float_as_uint(x[4 * w + i]) >> 24 & 0x80u) | 0x7Fu;
+                    out[w] |= (__builtin_isfinite(v) ? pack2_e4m3(v, 0.0f) & 0xFFu : nan) << (8 * i);
+                }
+            }
+        }
     }
 };
 
@@ -177,6 +199,10 @@ struct ProductShape {
     static constexpr int kAmax = kScales + (FP8 ? kScaleRing * kScaleBatch : 0);
     static constexpr size_t kLds = kAmax + (FP8 ? WN * MT * 4 : 0);   // then the tile table
 };
+
+// 1 / (1 + exp(-x)).  The reciprocal is within 1 ulp (the division costs ten
+// instructions, which a tile's epilogue pays up to 128 times a lane).
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // What one side of a tile loads in a stage.
 struct ProductSide {
@@ -704,77 +730,73 @@ struct ProductWg {
 
     // ---- results ----
 
-    // NB blocks of 16 columns (from `col` of the row on) of the lane's row as
-    // bf16.  Four blocks: the lanes of a row trade (a 4 x 4 transpose over the
-    // four lanes of a row, then the halves of two blocks) so that each store
-    // writes 64 bytes in a run.
-    template <int NB>
-    __device__ __forceinline__ void store_blocks(const f32x4 (&v)[NB], uint16_t *row, int cols, bool live, bool vector) const
+    // Four blocks of 16 columns of the lane's row as bf16.  The lanes of a row
+    // trade (a 4 x 4 transpose over the four lanes of a row, then the halves of
+    // two blocks) so that each store writes 64 bytes in a run.
+    __device__ __forceinline__ void store_blocks(const f32x4 (&v)[4], uint16_t *row, int cols, bool live, bool vector,
+                                                 int lane) const
     {
         const int g = lane >> 4;
-        uint32_t lo[NB], hi[NB];
+        uint32_t lo[4], hi[4];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
+        for (int j = 0; j < 4; ++j) {
             lo[j] = pack_bf16(v[j][0], v[j][1]);
             hi[j] = pack_bf16(v[j][2], v[j][3]);
         }
         if (!vector) {
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = 16 * j + 4 * g + i;
                     if (live && c < cols) row[c] = (uint16_t)((i < 2 ? lo[j] : hi[j]) >> (16 * (i & 1)));
                 }
-        } else if constexpr (NB == 4) {
-            uint32_t *w[2] = {lo, hi};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                swap_halves(w[h][0], w[h][2]);
-                swap_halves(w[h][1], w[h][3]);
-                swap_rows16(w[h][0], w[h][1]);
-                swap_rows16(w[h][2], w[h][3]);
-            }
-            // block g: bytes 0-15 in lo, hi [0, 1], 16-31 in lo, hi [2, 3]
-            swap_halves(lo[0], lo[2]);
-            swap_halves(hi[0], hi[2]);
-            swap_halves(lo[1], lo[3]);
-            swap_halves(hi[1], hi[3]);
-            const int c = 16 * (g & 1) + 8 * (g >> 1);
-            if (live && c < cols) *reinterpret_cast<u32x4 *>(row + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
-            if (live && c + 32 < cols) *reinterpret_cast<u32x4 *>(row + c + 32) = u32x4{lo[2], hi[2], lo[3], hi[3]};
-        } else {
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int c = 16 * j + 4 * g;
-                if (live && c < cols) *reinterpret_cast<u32x2 *>(row + c) = u32x2{lo[j], hi[j]};
-            }
+            return;
         }
+        uint32_t *w[2] = {lo, hi};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            swap_halves(w[h][0], w[h][2]);
+            swap_halves(w[h][1], w[h][3]);
+            swap_rows16(w[h][0], w[h][1]);
+            swap_rows16(w[h][2], w[h][3]);
+        }
+        // block g: bytes 0-15 in lo, hi [0, 1], 16-31 in lo, hi [2, 3]
+        swap_halves(lo[0], lo[2]);
+        swap_halves(hi[0], hi[2]);
+        swap_halves(lo[1], lo[3]);
+        swap_halves(hi[1], hi[3]);
+        const int c = 16 * (g & 1) + 8 * (g >> 1);
+        if (live && c < cols) *reinterpret_cast<u32x4 *>(row + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        if (live && c + 32 < cols) *reinterpret_cast<u32x4 *>(row + c + 32) = u32x4{lo[2], hi[2], lo[3], hi[3]};
     }
 
     template <int M>
-    __device__ __forceinline__ void store_tile(const Work<M> &k) const
+    __device__ __forceinline__ void store_tile(const Work<M> &k)
     {
         const int64_t ld = FORM == kFwd ? (EPI == kSwiglu ? a.N / 2 : a.N) : a.K;
         const bool vector = ld % 8 == 0 && (EPI != kSwigluGrad || a.N / 2 % 8 == 0) && ((uintptr_t)a.out & 15) == 0;
         const int64_t I = a.N / 2;
         constexpr int H = EPI == kPlain ? NF : NF / 2;       // blocks of output columns
-        constexpr int NB = H < 4 ? H : 4;
+        uint16_t *const first = a.out + ((FORM == kDw ? (int64_t)at.e * a.N : 0) + at.row0) * ld + at.n0;
+        // computed here, and not ahead of the tile and kept in registers that its sums need
+        int lane = this->lane;
+        asm volatile("" : "+v"(lane));
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int t = (m * S::WM + wm) * 16 + (lane & 15);
             const bool live = t < at.live_m;
-            uint16_t *row = a.out + (FORM == kDw ? (int64_t)at.e * a.N + at.row0 + t : at.row0 + t) * ld + at.n0;
 #pragma unroll
-            for (int q = 0; q < H / NB; ++q) {
-                const int c = (wn * H + q * NB) * 16;
-                f32x4 v[NB], w[NB];
+            for (int q = 0; q < H / 4; ++q) {
+                const int c = (wn * H + q * 4) * 16;
+                uint16_t *row = first + t * ld + c;
+                f32x4 v[4], w[4];
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     if constexpr (EPI == kPlain) {
-                        v[j] = k.acc[q * NB + j][m];
+                        v[j] = k.acc[q * 4 + j][m];
                     } else {
-                        const f32x4 gate = k.acc[q * NB + j][m], up = k.acc[H + q * NB + j][m];
+                        const f32x4 gate = k.acc[q * 4 + j][m], up = k.acc[H + q * 4 + j][m];
                         f32x4 d = {};
                         if constexpr (EPI == kSwigluGrad) {
                             const int col = c + 16 * j + 4 * (lane >> 4);
@@ -792,9 +814,9 @@ struct ProductWg {
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float s = 1.0f / (1.0f + __expf(-gate[i]));
+                            const float s = sigmoid(gate[i]);
                             if constexpr (EPI == kSwiglu) {
-                                v[j][i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i];
+                                v[j][i] = gate[i] * s * up[i];
                             } else {
                                 v[j][i] = d[i] * up[i] * (s * (1.0f + gate[i] * (1.0f - s)));
                                 w[j][i] = d[i] * (gate[i] * s);
@@ -802,8 +824,8 @@ struct ProductWg {
                         }
                     }
                 }
-                store_blocks<NB>(v, row + c, at.live_n - c, live, vector);
-                if constexpr (EPI == kSwigluGrad) store_blocks<NB>(w, row + I + c, at.live_n - c, live, vector);
+                store_blocks(v, row, at.live_n - c, live, vector, lane);
+                if constexpr (EPI == kSwigluGrad) store_blocks(w, row + I, at.live_n - c, live, vector, lane);
                 __builtin_amdgcn_sched_barrier(0);           // one group's temporaries at a time
             }
         }
@@ -825,7 +847,7 @@ struct ProductWg {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float g = k.acc[j][m][i];
-                        const float h = g / (1.0f + __expf(-g)) * k.acc[H + j][m][i];
+                        const float h = g * sigmoid(g) * k.acc[H + j][m][i];
                         k.acc[j][m][i] = h;
                         const uint32_t u = __float_as_uint(h) & 0x7FFFFFFFu;
                         top = u <= 0x7F800000u && u > top ? u : top;
@@ -855,7 +877,12 @@ struct ProductWg {
             const int64_t row = at.row0 + t;
             uint32_t w[H];
 #pragma unroll
-            for (int j = 0; j < H; ++j) w[j] = q.code4(k.acc[j][m][0], k.acc[j][m][1], k.acc[j][m][2], k.acc[j][m][3]);
+            for (int j = 0; j < H; ++j) {
+                const float h[4] = {k.acc[j][m][0], k.acc[j][m][1], k.acc[j][m][2], k.acc[j][m][3]};
+                uint32_t c[1];
+                q.template codes<1>(h, c);
+                w[j] = c[0];
+            }
             uint8_t *to = a.hq + row * I + at.n0 + wn * H * 16;
             const int g = lane >> 4;
             if constexpr (H == 4) {
@@ -907,7 +934,7 @@ __global__ __launch_bounds__(kProductThreads) void product_kernel(ProductArgs a,
         w.at = w.at_b;                                       // (B is not yet past this tile)
         const bool busy = w.wm * 16 < w.at.live_m;           // the wave has a live row
         const int blocks = busy ? (w.at.live_m + 63) / 64 : 0;
-        if (FORM == kDw || blocks == S::MF)                  // (gradients of the weights: all but a last tile are full)
+        if (blocks == S::MF)
             w.template run_tile<S::MF>();
         else if (blocks == 0)
             w.template run_tile<0>();
@@ -961,6 +988,16 @@ int launch_product_tiles(const ProductArgs &a, hipStream_t stream)
     return launch_status();
 }
 
+// Buffers of very many experts leave no room for their tile table beside the
+// smaller tiles' third stage (fp8: 1216 experts at 192 rows); 256 rows fit all.
+template <bool FP8, ProductForm FORM, int MT>
+bool product_fits(int32_t L)
+{
+    constexpr size_t kLdsBytes = 160 * 1024;
+    static_assert(ProductShape<FP8, FORM, 256>::kLds + CDL_MAX_LOCAL_EXPERTS * sizeof(int32_t) <= kLdsBytes, "largest tile");
+    return ProductShape<FP8, FORM, MT>::kLds + (size_t)L * sizeof(int32_t) <= kLdsBytes;
+}
+
 // Rows of a tile, 128, 192 or 256: the fewest rounds of the workgroups, weighed
 // by what a round costs (1.03, 1.33 and 1.59 us a stage where the matrix
 // instructions bound it).  The host sees the rows of the whole buffer only: an
@@ -973,20 +1010,20 @@ int launch_product_tiles(const ProductArgs &a, hipStream_t stream)
 // Padded buffers are mostly empty in decode, where the weights' bytes count
 // and three stages of them in LDS pay: 4 rows an expert, 32 experts, K = 7168,
 // N = 4096, bf16 307 / 307 / 328, fp8 162 / 161 / 175.
-template <ProductForm FORM, ProductEpilogue EPI>
+template <bool FP8, ProductForm FORM, ProductEpilogue EPI>
 int product_tile_rows(const ProductArgs &a)
 {
-    if (!a.seg) return 192;
+    if (!a.seg) return product_fits<FP8, FORM, 192>(a.L) ? 192 : 256;
     const int64_t width = FORM == kDx ? a.K : EPI == kPlain ? a.N : a.N / 2, cols = EPI == kPlain ? kProductNT : kProductNT / 2;
     const double tiles_n = (double)((width + cols - 1) / cols), r = (double)a.rows / a.L;
-    int best = 0;
+    int best = 256;
     double least = 0;
-    for (int mt = 128; mt <= 256; mt += 64) {
-        double tm = a.L == 1 ? (double)((a.rows + mt - 1) / mt) : r <= 0.8 * mt ? 1.0 : r / mt + 0.5;
-        const double tiles = tm * a.L * tiles_n, rounds = tiles <= kProductWgs ? 1.0 : tiles / kProductWgs;
-        const double whole = rounds <= 1.0 ? 1.0 : rounds <= 2.0 ? 2.0 : rounds;
-        const double cost = whole * (mt == 128 ? 1.03 : mt == 192 ? 1.33 : 1.59);
-        if (best == 0 || cost < least) {
+    for (int mt = 256; mt >= 128; mt -= 64) {
+        if (mt == 192 ? !product_fits<FP8, FORM, 192>(a.L) : mt == 128 && !product_fits<FP8, FORM, 128>(a.L)) continue;
+        const double tm = a.L == 1 ? (double)((a.rows + mt - 1) / mt) : r <= 0.8 * mt ? 1.0 : r / mt + 0.5;
+        const double rounds = tm * a.L * tiles_n / kProductWgs;
+        const double cost = (rounds <= 1.0 ? 1.0 : rounds <= 2.0 ? 2.0 : rounds) * (mt == 128 ? 1.03 : mt == 192 ? 1.33 : 1.59);
+        if (mt == 256 || cost < least) {
             best = mt;
             least = cost;
         }
@@ -1002,7 +1039,7 @@ int launch_product(const ProductArgs &a, hipStream_t stream)
     } else {
         // (an empty buffer: only the check of the counts is left)
         if (a.rows == 0 && !a.status) return CDL_OK;
-        const int mt = product_tile_rows<FORM, EPI>(a);
+        const int mt = product_tile_rows<FP8, FORM, EPI>(a);
         return mt == 256   ? launch_product_tiles<FP8, FORM, EPI, 256>(a, stream)
                : mt == 192 ? launch_product_tiles<FP8, FORM, EPI, 192>(a, stream)
                            : launch_product_tiles<FP8, FORM, EPI, 128>(a, stream);
