@@ -113,6 +113,15 @@ __device__ __forceinline__ double row_scale(double sum, int64_t H, float eps)
     return 1.0 / sqrt(sum / (double)H + (double)eps);
 }
 
+// A row's scale r in two parts.  The product of two bf16 (h w) is exact in fp32,
+// so that y = h w r is rounded once: as few values as can be land on the other
+// side of a border of fp8.
+struct RowScale {
+    float hi, lo;
+    __device__ __forceinline__ explicit RowScale(double r) : hi((float)r), lo((float)(r - (double)(float)r)) {}
+    __device__ __forceinline__ float times(float hw) const { return fmaf(hw, hi, hw * lo); }
+};
+
 // The scale of group g of row t (lanes of a group share it; lane 16 j of the
 // wave stores, or lane 0 a word of four groups, which begin at a multiple of
 // four: `first` is the wave's first group).
@@ -183,13 +192,13 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_kernel(NormArgs a)
             for (int i = 0; i < VEC; ++i) sum[0] = fmaf(h[j].at(i), h[j].at(i), sum[0]);
         double total[1];
         row_sums<1, WAVE>(sum, total, lds);
-        const float r = (float)row_scale(total[0], H, a.eps);
+        const RowScale r(row_scale(total[0], H, a.eps));
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
             const int64_t c = (int64_t)(tid + j * P) * VEC;
             float y[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = h[j].at(i) * w[j].at(i) * r;        // (the first product is exact)
+            for (int i = 0; i < VEC; ++i) y[i] = r.times(h[j].at(i) * w[j].at(i));
             if constexpr (FP8) {
                 if ((int64_t)((tid & ~(kWave - 1)) + j * P) * VEC >= H) break;       // (the whole wave)
                 uint32_t m = 0;
@@ -241,7 +250,7 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_long_kernel(NormArgs a)
         }
         double total[1];
         row_sums<1, false>(sum, total, lds);
-        const float r = (float)row_scale(total[0], H, a.eps);
+        const RowScale r(row_scale(total[0], H, a.eps));
         const uint16_t *src = a.res ? a.res_out : a.x;
         for (int64_t c0 = 0; c0 < H; c0 += kNormThreads * VEC) {
             const int64_t c = c0 + (int64_t)threadIdx.x * VEC;
@@ -256,7 +265,7 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_long_kernel(NormArgs a)
             }
             float y[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = h.at(i) * w.at(i) * r;
+            for (int i = 0; i < VEC; ++i) y[i] = r.times(h.at(i) * w.at(i));
             if constexpr (FP8) {
                 uint32_t m = 0;
 #pragma unroll

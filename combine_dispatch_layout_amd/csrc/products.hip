@@ -460,9 +460,10 @@ struct ProductWg {
             // An expert's row tiles share its rows evenly: workgroups that read the same weights keep step, so
             // that all but the first find them in the L2.  131072 rows of 128 experts, K = N = 4096: full tiles and
             // a rest 51% of the requests, 4.25 ms; evenly in blocks of 64 rows 4.15 ms; evenly 76%, 4.02 ms.
-            const int c = (int)g.count, mt = (c + MT - 1) / MT, q = c / mt, more = c - q * mt;
-            t.m0 = (int64_t)g.m * q + (g.m < more ? g.m : more);
-            t.live_m = q + (g.m < more ? 1 : 0);
+            const int c = (int)g.count, tiles = (c + MT - 1) / MT, mt = tiles > 1 ? tiles : 1, q = c / mt, more = c - q * mt;
+            const int m = g.m < mt ? g.m : mt - 1;
+            t.m0 = (int64_t)m * q + (m < more ? m : more);
+            t.live_m = q + (m < more ? 1 : 0);
         }
         t.n0 = (int64_t)g.n * kCols;
         t.row0 = FORM == kDw ? t.m0 : t.begin + t.m0;
@@ -959,7 +960,7 @@ inline int check_product(int64_t rows, int64_t K, int32_t L, int64_t N, const in
 {
     if (rows < 0 || K < 1 || N < 1 || L < 1 || L > CDL_MAX_LOCAL_EXPERTS) return CDL_ERR_BAD_SIZE;
     if (!seg && (cap < 0 || rows != (int64_t)L * cap)) return CDL_ERR_BAD_SIZE;
-    if (K > CDL_MAX_PRODUCT_WIDTH || N > CDL_MAX_PRODUCT_WIDTH || rows > INT32_MAX) return CDL_ERR_TOO_LARGE;
+    if (K > CDL_MAX_PRODUCT_WIDTH || N > CDL_MAX_PRODUCT_WIDTH || rows > INT32_MAX - 256) return CDL_ERR_TOO_LARGE;
     if (!counts) return CDL_ERR_NULL_POINTER;
     return CDL_OK;
 }

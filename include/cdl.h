@@ -650,9 +650,11 @@ int cdl_moe_layer_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
  * e * cap of a padded buffer of L * cap rows; a count that does not fit the
  * buffer is cut to what does and reported; rows of no expert are neither read
  * nor written.  Sums are taken in fp32 and rounded once.  K and N at most
- * CDL_MAX_PRODUCT_WIDTH; CDL_ERR_TOO_LARGE also where L times the output tiles
- * of one expert that owns the whole buffer (64 or 256 rows, 256 columns)
- * exceeds 2^31 - 257.
+ * CDL_MAX_PRODUCT_WIDTH, at most 2^31 - 257 rows; CDL_ERR_TOO_LARGE also where
+ * L times the output tiles of one expert that owns the whole buffer (128 to 256
+ * rows, 256 columns; SwiGLU 128) exceeds 2^31 - 257.  Every sum is taken in a
+ * fixed order: a result's bits depend on its row and weights alone.  counts and
+ * seg_indptr must not change while a call runs.
  */
 
 /*
