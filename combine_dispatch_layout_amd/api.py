@@ -25,6 +25,19 @@ and the local experts in MXFP4, or the whole layer for a few tokens:
     y = grouped_mxfp4(h, hs, w2_q, w2_s, lay.counts, lay.seg_indptr)   # [rows, H] bf16
     out = combine(y, lay.src2dst, topk_weights)
     out = moe_layer(x, topk_ids, topk_weights, w13, w2, expert_begin)  # few tokens
+
+or in the fp8 rows that the fp8 dispatches write, or in bf16 with gradients,
+behind the norm that makes the rows:
+
+    x, h = rms_norm(attention_out, norm_weight, residual)
+    lay, q, s = permute_fp8(x, topk_ids, expert_begin, num_local_experts)
+    a, a_s = grouped_swiglu_fp8(q, s, w13_8, w13_8s, lay.counts, lay.seg_indptr)
+    y = grouped_fp8(a, a_s, w2_8, w2_8s, lay.counts, lay.seg_indptr)
+
+    a = grouped_swiglu_bf16(rows, w13, lay.counts, lay.seg_indptr)
+    dgu = grouped_swiglu_bf16_grad(rows, w13, da, lay.counts, lay.seg_indptr)
+    drows = grouped_bf16_dx(dgu, w13, lay.counts, lay.seg_indptr)
+    dw13 = grouped_bf16_dw(dgu, rows, lay.counts, lay.seg_indptr)
 """
 from __future__ import annotations
 

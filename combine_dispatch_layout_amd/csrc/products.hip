@@ -18,6 +18,20 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 //
 // Depth runs along a row's bytes for operands taken by rows and across rows
 // for those taken by columns.
+//
+// One workgroup of 8 waves per CU walks its XCD's eighth of the tile list.  A
+// stage of 128 bytes of depth (64 rows of it by columns) is loaded straight to
+// LDS, one or two stages ahead of the matrix instructions, across tile borders.
+// With few rows an expert the weights' bytes bound the product, with many the
+// matrix instructions, at the rate that the card's power allows.
+//
+// Measured, one MI355X: 128 tokens over 32 of 256 experts, K = 7168, N = 4096,
+// 306 us in bf16 and 160 in fp8 (6.0 and 5.8 TB/s); 131072 rows of 128 uneven
+// experts, K = N = 4096, 3.9 to 4.1 ms and 2.45 to 2.6 ms (1.1 and 1.75 PFLOP/s;
+// a library product of one such bf16 matrix 1.47), the matrix unit 66 and 48%
+// busy at 1.65 and 1.9 GHz.  In bf16 a tile of 64 stages loses about 9.5 us to
+// its end there, 3.6 of them to its output's bytes; with every tile loading the
+// same lines, which stay in the L2, it takes 3.4 ms.
 // ---------------------------------------------------------------------------
 // The scale and codes of a group of 128 values in fp8 from its largest
 // magnitude (over its values that are not NaN; infinite if one is): the

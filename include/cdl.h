@@ -10,8 +10,8 @@
  *
  *   layout  (routing histogram, prefix sum, stable slot ranks)
  *     -> dispatch (row scatter: normal / low-latency padded / fp8 groups)
- *     -> [expert computation: outside this library, or the grouped MXFP4
- *         product below]
+ *     -> [expert computation: outside this library, or the grouped bf16, fp8 and
+ *         MXFP4 products below]
  *     -> combine (gather + top-k-weighted sum per token, fp32 accumulation)
  *
  * Conventions shared by every entry point:
@@ -621,8 +621,8 @@ size_t cdl_moe_layer_workspace_size(int64_t T, int32_t k, int64_t I, int32_t L);
  *   ws, ws_bytes      cdl_moe_layer_workspace_size bytes, 16-byte aligned, no
  *                     initialisation needed; calls that overlap need their own
  * T <= CDL_MOE_LAYER_MAX_TOKENS and T * k <= 4096 (CDL_ERR_UNSUPPORTED
- * otherwise: larger batches of MXFP4 weights take the permute, the grouped
- * products and the combine; this library has no grouped product of bf16 weights); T * H and T' * k * I at most 2^31 - 9, T' = max(T, 2 min(T, 2))
+ * otherwise: larger batches take the permute, the grouped products and the
+ * combine); T * H and T' * k * I at most 2^31 - 9, T' = max(T, 2 min(T, 2))
  * (CDL_ERR_TOO_LARGE); H % 8 == 0 and I % 8 == 0; x, w13 and w2 16-byte
  * aligned, out 4-byte aligned.  The sums are taken in a fixed order: the
  * result is deterministic.
