@@ -1064,6 +1064,18 @@ def _have(t, name: str, dtype, shape, dev) -> None:
         _same_device(dev, **{name: t})
 
 
+def _apart(t: Optional[torch.Tensor], name: str, same: Tuple[str, ...] = (), **others) -> None:
+    """A given output shares no memory with the call's other arrays, except
+    that it may be one of those named in `same`, whole."""
+    if t is None:
+        return
+    at, end = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    for other, u in others.items():
+        if u is not None and u.data_ptr() < end and at < u.data_ptr() + u.numel() * u.element_size():
+            if other not in same or u.data_ptr() != at:
+                raise ValueError("%s overlaps %s" % (name, other))
+
+
 def _groups(rows: torch.Tensor, name: str, L: int, counts, seg_indptr, status):
     """Checked rows of the grouped products, [rows, n] with seg_indptr and
     [L, cap, n] without: (number of rows, cap)."""
@@ -1109,6 +1121,8 @@ def _bf16_product(what, x, w, counts, seg_indptr, out, status, width_of, extra=N
     if extra is not None:
         _have(extra, "dh", torch.bfloat16, (*x.shape[:-1], n), x.device)
         more = (_ptr(extra),)
+    if out is not None:
+        _apart(out, "out", x=x, w=w, dh=extra)
     out = _product_rows(out, "out", x, width)
     _same_device(x.device, w=w)
     _launch(what, x.device, _ptr(x), rows, K, _ptr(w), L, n, *more, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out),
@@ -1163,6 +1177,8 @@ def grouped_bf16_dx(dy: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg
     if dy.dim() < 2 or dy.shape[-1] != N:
         raise ValueError("dy must have rows of N = %d elements, got %s" % (N, tuple(dy.shape)))
     rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
+    if out is not None:
+        _apart(out, "out", dy=dy, w=w)
     out = _product_rows(out, "out", dy, K)
     _same_device(dy.device, w=w)
     _launch("cdl_grouped_bf16_dx", dy.device, _ptr(dy), rows, N, _ptr(w), L, K, _ptr(counts), _ptr(seg_indptr), cap,
@@ -1184,7 +1200,9 @@ def grouped_bf16_dw(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, seg
     N, K = dy.shape[-1], x.shape[-1]
     if out is None:
         out = torch.empty(L, N, K, dtype=torch.bfloat16, device=dy.device)
-    _have(out, "out", torch.bfloat16, (L, N, K), dy.device)
+    else:
+        _have(out, "out", torch.bfloat16, (L, N, K), dy.device)
+        _apart(out, "out", dy=dy, x=x)
     _same_device(dy.device, x=x)
     _launch("cdl_grouped_bf16_dw", dy.device, _ptr(dy), _ptr(x), rows, N, K, L, _ptr(counts), _ptr(seg_indptr), cap,
             _ptr(out), _ptr(status))
@@ -1216,6 +1234,8 @@ def grouped_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scal
     scale_flags format), w_q [L, N, K] and w_scales [L, ceil(N / 128), K / 128]
     as quant_fp8_blocks does.  Rows and counts as for grouped_bf16."""
     L, N, K, rows, cap = _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status)
+    if out is not None:
+        _apart(out, "out", q=q, scales=scales, w_q=w_q, w_scales=w_scales)
     out = _product_rows(out, "out", q, N)
     _launch("cdl_grouped_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, K, _ptr(w_q), _ptr(w_scales), L, N,
             _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status))
@@ -1234,6 +1254,8 @@ def grouped_swiglu_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor,
     I = _halves(N)
     if I % FP8_GROUP:
         raise CdlError(-3, "grouped_swiglu_fp8 (I must be a multiple of %d)" % FP8_GROUP)
+    _apart(out_q, "out_q", q=q, scales=scales, w_q=w_q, w_scales=w_scales, out_scales=out_scales)
+    _apart(out_scales, "out_scales", q=q, scales=scales, w_q=w_q, w_scales=w_scales)
     if out_q is None:
         out_q = torch.empty(*q.shape[:-1], I, dtype=torch.uint8, device=q.device)
     _need(out_q, "out_q", torch.uint8, (*q.shape[:-1], I))
@@ -1268,6 +1290,8 @@ def quant_fp8_blocks(w: torch.Tensor, out_q: Optional[torch.Tensor] = None,
     if K < 1 or K % FP8_GROUP:
         raise CdlError(-3, "quant_fp8_blocks (K must be a multiple of %d)" % FP8_GROUP)
     lead = w.shape[:-2]
+    _apart(out_q, "out_q", w=w, out_scales=out_scales)
+    _apart(out_scales, "out_scales", w=w)
     if out_q is None:
         out_q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
     if out_scales is None:
@@ -1296,6 +1320,8 @@ def dequant_fp8(q: torch.Tensor, scales: torch.Tensor, scale_flags: int = 0,
     rows = q.numel() // H
     rpm = q.shape[-2]
     _check_scale_buffer(scales, rows, H, scale_flags, rpm)
+    if out is not None:
+        _apart(out, "out", q=q, scales=scales)
     out = _product_rows(out, "out", q, H)
     _same_device(q.device, scales=scales)
     _launch("cdl_dequant_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, H, rpm, _ptr(out))
@@ -1318,8 +1344,12 @@ def _norm_args(x, weight, eps) -> Tuple[int, int]:
     return x.numel() // H, H
 
 
-def _norm_residual(x, residual, residual_out):
+def _norm_residual(x, weight, residual, out, residual_out):
     """The checked residual_out, new where there is none; None without residual."""
+    if out is not None:
+        _apart(out, "out", ("x", "residual"), x=x, weight=weight, residual=residual, residual_out=residual_out)
+    if residual_out is not None:
+        _apart(residual_out, "residual_out", ("x", "residual"), x=x, weight=weight, residual=residual)
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs residual")
@@ -1343,7 +1373,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     normed); then returns (out, h), otherwise out.  out and residual_out may be
     x or residual itself."""
     T, H = _norm_args(x, weight, eps)
-    residual_out = _norm_residual(x, residual, residual_out)
+    residual_out = _norm_residual(x, weight, residual, out, residual_out)
     out = _same_rows(out, "out", x)
     _launch("cdl_rms_norm", x.device, _ptr(x), _ptr(residual), _ptr(weight), float(eps), T, H, _ptr(out),
             _ptr(residual_out))
@@ -1362,9 +1392,13 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         raise ValueError("x must be [T, H]")
     if H % FP8_GROUP:
         raise CdlError(-3, "rms_norm_fp8 (H must be a multiple of %d)" % FP8_GROUP)
-    residual_out = _norm_residual(x, residual, residual_out)
+    residual_out = _norm_residual(x, weight, residual, out, residual_out)
     if out is not None:
         out = _same_rows(out, "out", x)
+    if out_q is not None or out_scales is not None:
+        rest = dict(x=x, weight=weight, residual=residual, out=out, residual_out=residual_out)
+        _apart(out_q, "out_q", out_scales=out_scales, **rest)
+        _apart(out_scales, "out_scales", **rest)
     if out_q is None:
         out_q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
     else:
@@ -1398,6 +1432,11 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
     _have(dy, "dy", torch.bfloat16, h.shape, h.device)
     if dresidual is not None:
         _have(dresidual, "dresidual", torch.bfloat16, h.shape, h.device)
+    if out is not None or dweight is not None or workspace is not None:
+        rest = dict(dy=dy, h=h, weight=weight, dresidual=dresidual)
+        _apart(out, "out", ("dy", "h", "dresidual"), dweight=dweight, workspace=workspace, **rest)
+        _apart(dweight, "dweight", workspace=workspace, **rest)
+        _apart(workspace, "workspace", **rest)
     out = _same_rows(out, "out", h)
     if dweight is None:
         dweight = torch.empty(H, dtype=torch.float32, device=h.device)

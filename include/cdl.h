@@ -654,7 +654,8 @@ int cdl_moe_layer_mxfp4(const uint16_t *x, int64_t T, int64_t H, int32_t k,
  * L times the output tiles of one expert that owns the whole buffer (128 to 256
  * rows, 256 columns; SwiGLU 128) exceeds 2^31 - 257.  Every sum is taken in a
  * fixed order: a result's bits depend on its row and weights alone.  counts and
- * seg_indptr must not change while a call runs.
+ * seg_indptr must not change while a call runs; no output may overlap an operand,
+ * and the experts' segments may not overlap each other.
  */
 
 /*

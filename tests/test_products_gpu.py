@@ -590,3 +590,54 @@ def test_training_pass_of_the_experts():
         slope = float((loss(*hi) - loss(*lo)) / (2 * step))
         along = float((got.double() * d).sum())
         assert abs(along - slope) < 3 * R.BF16 * float(got.double().norm() * d.norm()) ** 1.0, (which, along, slope)
+
+
+@pytest.mark.parametrize("flags,packed", [(0, False), (7, True)])
+def test_fp8_padded_buffers_of_many_experts(flags, packed):
+    """2000 experts, whose tile table leaves no room for the smaller tiles' third stage."""
+    announce("padded fp8 products of 2000 experts, flags %d" % flags)
+    L, K, N, g = 2000, 256, 256, gen(flags)
+    counts = [(5 * e) % 4 for e in range(L)]
+    r = Rows(counts, True)
+    q, s, p = fp8_rows(g, r, K, flags)
+    wq, ws = fp8_weights(g, L, N, K)
+    y = cdl.grouped_fp8(r.shape(q), s, wq, ws, r.c, scale_flags=flags).view(r.n, N)
+    hq, hs = cdl.grouped_swiglu_fp8(r.shape(q), s, wq, ws, r.c, scale_flags=flags)
+    hq, hp = hq.view(r.n, N // 2), R.scales(hs, flags, r.n, 1, r.cap)
+    for e, at in list(r.each())[:20] + list(r.each())[-20:]:
+        v, err = R.fp8_product(q[at], p[at], wq[e], ws[e])
+        R.assert_within(y[at], v, R.to_bf16_bound(v, err), e)
+        h, dh = R.swiglu(v[:, :N // 2], err[:, :N // 2], v[:, N // 2:], err[:, N // 2:])
+        check_fp8_values(h, dh, hq[at], hp[at], bool(flags & 1))
+
+
+def test_outputs_over_operands_are_refused():
+    announce("overlapping outputs")
+    g, T, K = gen(3), 12, 128
+    x, w = rand(g, T, K), rand(g, 1, K, K)
+    c, seg = torch.tensor([T], dtype=torch.int32, device=DEV), torch.tensor([0, T], device=DEV)
+    q = torch.zeros(T, K, dtype=torch.uint8, device=DEV)
+    s = torch.ones(T, 1, device=DEV)
+    wq, ws = cdl.quant_fp8_blocks(rand(g, 1, 2 * K, K))
+    both = torch.zeros(T + 1, K, dtype=BF, device=DEV)
+    rows = torch.zeros(T, K, dtype=BF, device=DEV)
+    ws32 = torch.zeros(cdl.rms_norm_grad_workspace_size(T, K) // 4, device=DEV)
+    for call in (lambda: cdl.grouped_bf16(x, w, c, seg, out=x),
+                 lambda: cdl.grouped_bf16(both[:T], w, c, seg, out=both[1:]),
+                 lambda: cdl.grouped_swiglu_bf16(x, rand(g, 1, 2 * K, K), c, seg, out=x),
+                 lambda: cdl.grouped_swiglu_bf16_grad(x, w, rows[:, :K // 2].contiguous(), c, seg, out=x),
+                 lambda: cdl.grouped_bf16_dx(x, w, c, seg, out=x),
+                 lambda: cdl.grouped_bf16_dw(big := rand(g, K, K), big, torch.tensor([K], dtype=torch.int32, device=DEV),
+                                             torch.tensor([0, K], device=DEV), out=big.view(1, K, K)),
+                 lambda: cdl.grouped_fp8(both[:T // 2].view(torch.uint8).view(T, K), s, wq, ws, c, seg,
+                                         out=both[:T]),
+                 lambda: cdl.grouped_swiglu_fp8(q, s, wq, ws, c, seg, out_q=q),
+                 lambda: cdl.grouped_swiglu_fp8(q, s, wq, ws, c, seg, out_scales=s),
+                 lambda: cdl.rms_norm(x, w[0, 0], rows, out=both[:T], residual_out=both[:T]),
+                 lambda: cdl.rms_norm(both[:T], w[0, 0], out=both[1:]),
+                 lambda: cdl.rms_norm_fp8(x, w[0, 0], out_q=x.view(torch.uint8).view(2 * T, K)[:T]),
+                 lambda: cdl.rms_norm_grad(both[:T], x, w[0, 0], out=both[1:]),
+                 lambda: cdl.rms_norm_grad(rows, x, w[0, 0], dweight=ws32[:K], workspace=ws32),
+                 lambda: cdl.dequant_fp8(both[:T // 2].view(torch.uint8).view(T, K), s, out=both[:T])):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
