@@ -27,7 +27,7 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 //
 // Measured, one MI355X: 128 tokens over 32 of 256 experts, K = 7168, N = 4096,
 // 306 us in bf16 and 160 in fp8 (6.0 and 5.8 TB/s); 131072 rows of 128 uneven
-// experts, K = N = 4096, 3.9 to 4.1 ms and 2.45 to 2.6 ms (1.1 and 1.75 PFLOP/s;
+// experts, K = N = 4096, 3.9 to 4.2 ms and 2.45 to 2.6 ms (1.1 and 1.75 PFLOP/s;
 // a library product of one such bf16 matrix 1.47), the matrix unit 66 and 48%
 // busy at 1.65 and 1.9 GHz.  In bf16 a tile of 64 stages loses about 9.5 us to
 // its end there, 3.6 of them to its output's bytes; with every tile loading the
