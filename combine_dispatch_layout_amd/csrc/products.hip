@@ -244,6 +244,15 @@ struct ProductWg {
     static constexpr int R = FP8 ? 2 : 4, D = R - 1;           // fragments of A in registers, read ahead
     static_assert(NF % R == 0, "a fragment's registers do not depend on the stage");
     static constexpr bool kUpByUnit = EPI != kPlain;           // A's units alternate between gate and up rows
+    // fp8 values multiplied as bf16 ones, which hold them exactly.  The fp8 instructions (of either depth) drop what
+    // lies below 2^-13 of the largest of 8 neighbouring products; a result rounded to bf16 does not show it, but h,
+    // quantised again, lands on other codes: of an expert step of 4096 tokens 0.16% of them, so 0.001%, and the step's
+    // result is off by 0.0024 of 64 bits instead of 0.0026 (0.0017 without the bf16 rows between product and combine).
+    // It costs half the matrix rate and a conversion: gate/up products of 131072 rows of 128 experts, K = N = 4096,
+    // 2.75 -> 4.25 ms; of 4096 rows of 32 experts, K = 7168, 235 -> 345 us; of 128 such rows in the padded buffer
+    // 165 -> 168 us.
+    static constexpr bool kAsBf16 = FP8 && EPI == kSwiglu;
+    static constexpr int kSteps = kAsBf16 ? 4 : FP8 ? 1 : 2;   // matrix instructions per pair of fragments and stage
 
     const ProductArgs a;
     const int32_t *const ends;
@@ -271,6 +280,11 @@ struct ProductWg {
         i32x8 fa[R], fb[M];
         f32x4 part[M];                       // fp8: the sums of a stage of the A fragment before, and their scales
         float part_s[M];
+        // a stage's fragments of B as bf16, converted once; where the registers do not hold all of them, the rest for
+        // every fragment of A
+        static constexpr int kHeld = M < 4 ? 4 : 2;
+        v8bf16 wide[kAsBf16 ? M : 1][kHeld];
+        v8bf16 av[2];                        // of A, converted one step ahead
     };
 
     __device__ __forceinline__ ProductWg(const ProductArgs &args, uint8_t *l, const int32_t *e, int tm, int tn, int32_t end,
@@ -608,6 +622,19 @@ struct ProductWg {
         return *reinterpret_cast<const float *>(p + block * 16 + (s & 3) * 4);
     }
 
+    // 8 of a fragment's fp8 values (x = 0 to 3) as bf16; both operands of a product take the same x, so that the depths
+    // agree.
+    static __device__ __forceinline__ v8bf16 as_bf16(const i32x8 &f, int x, bool again = false)
+    {
+        typedef __bf16 v2bf16 __attribute__((ext_vector_type(2)));
+        int lo = f[2 * x], hi = f[2 * x + 1];
+        if (again) asm volatile("" : "+v"(lo), "+v"(hi));      // not the registers of an earlier conversion
+        const v2bf16 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false),
+                     b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true),
+                     c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false),
+                     d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+        return v8bf16{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
     static __device__ __forceinline__ f32x4 mma(const i32x8 &x, const i32x8 &y, f32x4 c, int half)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, half_of(x, half)),
@@ -667,7 +694,7 @@ struct ProductWg {
             }
             Units u;
             // matrix instructions per fragment, between the barriers, after them
-            constexpr int kPer = FP8 ? M : 2 * M, kBetween = (NF - D - 1) * kPer, kAfter = D * kPer;
+            constexpr int kPer = kSteps * M, kBetween = (NF - D - 1) * kPer, kAfter = D * kPer;
             static_assert(NF - D > 1, "steps between the barriers");
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
@@ -684,7 +711,19 @@ struct ProductWg {
 #pragma unroll
                 for (int x = 0; x < kPer; ++x) {
                     const int m = x % M;
-                    if constexpr (FP8) {
+                    if constexpr (kAsBf16) {
+                        constexpr int kHeld = Work<M>::kHeld;
+                        const int q = x / M;
+                        if (q == 0) add_part(k, (n + NF - 1) % NF, m);
+                        if (n == 0 && x == 0) k.wide[0][0] = as_bf16(k.fb[0], 0);
+                        const v8bf16 bv = q < kHeld ? k.wide[m][q] : as_bf16(k.fb[m], q, true);
+                        k.part[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.av[q & 1], bv, q == 0 ? f32x4{} : k.part[m], 0, 0, 0);
+                        // behind the matrix instruction: what the next one, and the next step, take
+                        if (m == 0) k.av[(q + 1) & 1] = as_bf16(k.fa[(q < 3 ? n : n + 1) % R], (q + 1) & 3);
+                        if (n == 0 && x + 1 < kPer && (x + 1) / M < kHeld)
+                            k.wide[(x + 1) % M][(x + 1) / M] = as_bf16(k.fb[(x + 1) % M], (x + 1) / M);
+                        k.part_s[m] = n >= NF / 2 ? sc2[m] : sc[m];
+                    } else if constexpr (FP8) {
                         add_part(k, (n + NF - 1) % NF, m);
                         k.part[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k.fa[n % R], k.fb[m], f32x4{}, 0, 0, 0, 0, 0, 0);
                         k.part_s[m] = EPI != kPlain && n >= NF / 2 ? sc2[m] : sc[m];
@@ -694,7 +733,9 @@ struct ProductWg {
                     __builtin_amdgcn_sched_barrier(0);
                     // B's registers take the next stage's as soon as they are used up
                     if (n == NF - 1) {
-                        if constexpr (FP8)
+                        if constexpr (kAsBf16) {
+                            if (x / M == (Work<M>::kHeld == 4 ? 0 : 3)) k.fb[m] = b_fragment(next_b, m);
+                        } else if constexpr (FP8)
                             k.fb[m] = b_fragment(next_b, m);
                         else
                             k.fb[m] = x < M ? join(b_half(next_b, m, 0), half_of(k.fb[m], 1)) : join(half_of(k.fb[m], 0), b_half(next_b, m, 1));
@@ -726,6 +767,7 @@ struct ProductWg {
                 k.part[j] = f32x4{};
                 k.part_s[j] = 0.0f;
             }
+            if constexpr (kAsBf16) k.av[0] = as_bf16(k.fa[0], 0);
         }
         for (int s = 0; s < at.stages; ++s) {
             run_stage<M>(k, s);
@@ -1032,13 +1074,16 @@ int product_tile_rows(const ProductArgs &a)
     const int64_t width = FORM == kDx ? a.K : EPI == kPlain ? a.N : a.N / 2, cols = EPI == kPlain ? kProductNT : kProductNT / 2;
     const double tiles_n = (double)((width + cols - 1) / cols), r = (double)a.rows / a.L;
     int best = 256;
-    double least = 0;
-    for (int mt = 256; mt >= 128; mt -= 64) {
+    double least = 1e300;
+    // Quantised SwiGLU takes 256 rows only where nothing else fits: their bf16 fragments do not (131072 rows of 128
+    // experts, K = N = 4096: 128 / 192 / 256 rows 4.97 / 4.25 / 5.73 ms).
+    constexpr int kMost = FP8 && EPI == kSwiglu ? 192 : 256;
+    for (int mt = product_fits<FP8, FORM, kMost>(a.L) ? kMost : 256; mt >= 128; mt -= 64) {
         if (mt == 192 ? !product_fits<FP8, FORM, 192>(a.L) : mt == 128 && !product_fits<FP8, FORM, 128>(a.L)) continue;
         const double tm = a.L == 1 ? (double)((a.rows + mt - 1) / mt) : r <= 0.8 * mt ? 1.0 : r / mt + 0.5;
         const double rounds = tm * a.L * tiles_n / kProductWgs;
         const double cost = (rounds <= 1.0 ? 1.0 : rounds <= 2.0 ? 2.0 : rounds) * (mt == 128 ? 1.03 : mt == 192 ? 1.33 : 1.59);
-        if (mt == 256 || cost < least) {
+        if (cost < least) {
             best = mt;
             least = cost;
         }

@@ -737,6 +737,8 @@ int cdl_grouped_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, i
  * every expert; h = g / (1 + exp(-g)) * u in fp32, quantised in groups of 128
  * as by the fp8 dispatch into out_q [rows, I] (16-byte aligned) and out_scales
  * in the scale_flags format of the input: the operand of the down product.
+ * Here every sum is fp32 and nothing is dropped (the values are multiplied as
+ * bf16, which holds them exactly): h lands on the codes of fp32 sums.
  * I % 128 == 0; the rest as cdl_grouped_fp8.
  */
 int cdl_grouped_swiglu_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, int64_t rows, int64_t K,
