@@ -86,15 +86,14 @@ __device__ __forceinline__ double wave_sum(double v)
     return v;
 }
 
-// Sums over a row's threads: a wave, or the workgroup's four.  A thread's own
-// sum is fp32; over the threads it is taken in 64 bits, whose few additions
-// cost nothing beside the row's loads: the last ones of a tree carry most of
-// its rounding, and an error of r moves a whole row across fp8's borders.
+// Sums over a row's threads: a wave, or the workgroup's four, in 64 bits, whose
+// additions cost nothing beside the row's loads: the last ones of a tree carry
+// most of its rounding.
 template <int N, bool WAVE>
-__device__ __forceinline__ void row_sums(const float (&v)[N], double (&s)[N], double *lds)
+__device__ __forceinline__ void row_sums(const double (&v)[N], double (&s)[N], double *lds)
 {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = wave_sum((double)v[i]);
+    for (int i = 0; i < N; ++i) s[i] = wave_sum(v[i]);
     if constexpr (!WAVE) {
         const int wave = threadIdx.x / kWave;
         if (threadIdx.x % kWave == 0) {
@@ -106,6 +105,18 @@ __device__ __forceinline__ void row_sums(const float (&v)[N], double (&s)[N], do
         for (int i = 0; i < N; ++i) s[i] = (lds[i] + lds[N + i]) + (lds[2 * N + i] + lds[3 * N + i]);
         __syncthreads();
     }
+}
+
+// s + the squares of a unit, in 64 bits (a conversion and an addition an
+// element, hidden behind the row's loads: 4096 x 7168 to fp8 39 us either way):
+// an error of r moves values of a whole row across fp8's borders, and a sum in 32
+// bits loses small squares beside large ones, and the range of rows beyond 2^64.
+template <int VEC>
+__device__ __forceinline__ double add_squares(const Unit<VEC> &h, double s)
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s = fma((double)h.at(i), (double)h.at(i), s);
+    return s;
 }
 
 // 1 / sqrt(sum / H + eps)
@@ -186,11 +197,9 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_kernel(NormArgs a)
             const int64_t c = (int64_t)(tid + j * P) * VEC;
             if (c < H) w[j].load(a.w + c);
         }
-        float sum[1] = {0.0f};
+        double sum[1] = {0.0};
 #pragma unroll
-        for (int j = 0; j < NU; ++j)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) sum[0] = fmaf(h[j].at(i), h[j].at(i), sum[0]);
+        for (int j = 0; j < NU; ++j) sum[0] = add_squares(h[j], sum[0]);
         double total[1];
         row_sums<1, WAVE>(sum, total, lds);
         const RowScale r(row_scale(total[0], H, a.eps));
@@ -234,7 +243,7 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_long_kernel(NormArgs a)
     const int64_t H = a.H;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * H;
-        float sum[1] = {0.0f};
+        double sum[1] = {0.0};
         for (int64_t c = (int64_t)threadIdx.x * VEC; c < H; c += kNormThreads * VEC) {
             Unit<VEC> h;
             h.load(a.x + row + c);
@@ -244,10 +253,7 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_long_kernel(NormArgs a)
                 h.add(r);
                 h.store(a.res_out + row + c);
             }
-            float part = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) part = fmaf(h.at(i), h.at(i), part);
-            sum[0] += part;
+            sum[0] = add_squares(h, sum[0]);
         }
         double total[1];
         row_sums<1, false>(sum, total, lds);
@@ -310,6 +316,15 @@ struct NormGradArgs {
     int32_t G;
 };
 
+// s + a unit's sums of h^2 and d h, in 64 bits as the norm's.
+template <int VEC>
+__device__ __forceinline__ void add_gradient_sums(const Unit<VEC> &h, const Unit<VEC> &g, const Unit<VEC> &w, double (&s)[2])
+{
+    s[0] = add_squares(h, s[0]);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[1] = fma((double)(g.at(i) * w.at(i)), (double)h.at(i), s[1]);
+}
+
 template <int VEC, int NU>
 __global__ __launch_bounds__(kNormThreads) void rms_norm_grad_kernel(NormGradArgs a)
 {
@@ -356,15 +371,9 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_grad_kernel(NormGradArg
                 if (c < H) dr[j].load(a.dres + t * H + c);
             }
         }
-        float s[2] = {0.0f, 0.0f};
+        double s[2] = {0.0, 0.0};
 #pragma unroll
-        for (int j = 0; j < NU; ++j)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float x = hh[j].at(i);
-                s[0] = fmaf(x, x, s[0]);
-                s[1] = fmaf(gg[j].at(i) * w[j].at(i), x, s[1]);
-            }
+        for (int j = 0; j < NU; ++j) add_gradient_sums(hh[j], gg[j], w[j], s);
         double total[2];
         row_sums<2, false>(s, total, lds);
         const double rd = row_scale(total[0], H, a.eps);
@@ -401,21 +410,13 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_grad_stats_kernel(NormG
 {
     __shared__ double lds[8];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        float s[2] = {0.0f, 0.0f};
+        double s[2] = {0.0, 0.0};
         for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += kNormThreads * VEC) {
             Unit<VEC> h, g, w;
             h.load(a.h + t * a.H + c);
             g.load(a.dy + t * a.H + c);
             w.load(a.w + c);
-            float p[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float x = h.at(i);
-                p[0] = fmaf(x, x, p[0]);
-                p[1] = fmaf(g.at(i) * w.at(i), x, p[1]);
-            }
-            s[0] += p[0];
-            s[1] += p[1];
+            add_gradient_sums(h, g, w, s);
         }
         double total[2];
         row_sums<2, false>(s, total, lds);

@@ -770,8 +770,9 @@ int cdl_dequant_fp8(const uint8_t *q, const void *scales, int32_t scale_flags, i
  * cdl_rms_norm -- the norm before a layer, with the residual's addition:
  *   h[t] = residual ? bf16_rne(x[t] + residual[t]) : x[t]
  *   out[t, c] = bf16_rne(h[t, c] / sqrt(mean(h[t]^2) + eps) * weight[c])
- * in fp32.  h is rounded before it is normed: the norm is that of the rows the
- * residual path keeps, as by two separate calls.
+ * in fp32, the sum of squares in 64 bits (rows of any bf16 size).  h is rounded
+ * before it is normed: the norm is that of the rows the residual path keeps, as
+ * by two separate calls.
  *   x, residual   in  [T, H] bf16 (residual may be NULL)
  *   weight        in  [H] bf16
  *   out           out [T, H] bf16

@@ -1,0 +1,45 @@
+"""The root-mean-square norm where ordinary rows do not tell a mistake: squares
+of very unlike size, and weights whose products leave fp32's range."""
+import pytest
+import torch
+
+import combine_dispatch_layout_amd as cdl
+import products_ref as R
+from gpu_util import DEV, announce
+from test_products_gpu import BF, gen, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H", [512, 1024, 2048, 4096, 7168, 8320])
+def test_sums_of_unlike_squares_keep_the_small_ones(H):
+    """Of every 8 elements one is 2^12 to 2^13 and seven are near 1: an fp32 sum loses most of the squares of the seven
+    beside 2^24 and more, some 2e-7 of the whole, and with it the codes of the values that lie that near to a border between two.  The codes
+    have to be those of the fp32 values nearest to 64-bit ones: a value's own rounding is all that they may go by."""
+    announce("norm of unlike squares H=%d" % H)
+    g, T = gen(H), (1 << 23) // H
+    x = 1 + 0.25 * torch.randn(T, H, generator=g, device=DEV)
+    x[:, ::8] = 4096 * (1 + torch.rand(T, 1, generator=g, device=DEV))             # (a scale of every row's own)
+    x, w = x.to(BF), (1 + 0.3 * torch.randn(H, generator=g, device=DEV)).to(BF)
+    q, s = cdl.rms_norm_fp8(x, w, scale_flags=cdl.FP8_SCALE_UE8M0)
+    h = x.double()
+    y = h * w.double() / torch.sqrt(h.pow(2).mean(-1, keepdim=True) + 1e-6)
+    want = (y.unflatten(-1, (-1, 128)) / s.double().unsqueeze(-1)).flatten(-2).float().to(torch.float8_e4m3fn)
+    assert int((q != want.view(torch.uint8)).sum()) == 0
+
+
+@pytest.mark.parametrize("power", [-100, 100])
+@pytest.mark.parametrize("H", [100, 512, 2592, 9000, 9001])
+def test_rows_far_from_one(H, power):
+    """Rows of about 2^power, whose squares 32 bits do not hold, give what rows of about 1 give, and their gradient
+    that of those times 2^-power."""
+    announce("norm of rows of 2^%d H=%d" % (power, H))
+    g, T = gen(H), 6
+    x, w, dy = rand(g, T, H), rand(g, H, scale=0.3) + 1, rand(g, T, H)
+    far = x * 2.0 ** power
+    assert torch.equal(cdl.rms_norm(far, w, eps=0.0), cdl.rms_norm(x, w, eps=0.0))
+    dx, dw = cdl.rms_norm_grad(dy, x, w, 0.0)
+    fx, fw = cdl.rms_norm_grad(dy, far, w, 0.0)
+    assert torch.equal(fw, dw) and torch.equal(fx.float() * 2.0 ** power, dx.float())
+
+
