@@ -14,8 +14,8 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("H", [512, 1024, 2048, 4096, 7168, 8320])
 def test_sums_of_unlike_squares_keep_the_small_ones(H):
     """Of every 8 elements one is 2^12 to 2^13 and seven are near 1: an fp32 sum loses most of the squares of the seven
-    beside 2^24 and more, some 2e-7 of the whole, and with it the codes of the values that lie that near to a border between two.  The codes
-    have to be those of the fp32 values nearest to 64-bit ones: a value's own rounding is all that they may go by."""
+    beside 2^24 and more, some 2e-7 of the whole, and with it the codes of the values that lie that near to a border
+    between two.  The codes have to be those of the fp32 values nearest to 64-bit ones."""
     announce("norm of unlike squares H=%d" % H)
     g, T = gen(H), (1 << 23) // H
     x = 1 + 0.25 * torch.randn(T, H, generator=g, device=DEV)
@@ -43,3 +43,38 @@ def test_rows_far_from_one(H, power):
     assert torch.equal(fw, dw) and torch.equal(fx.float() * 2.0 ** power, dx.float())
 
 
+@pytest.mark.parametrize("H", [100, 512, 2048, 9000, 9001])
+def test_infinite_weights_and_products_beyond_fp32(H):
+    announce("norm with infinite weights and large products H=%d" % H)
+    g, T = gen(H), 5
+    x, w = rand(g, T, H), rand(g, H, scale=0.3) + 1
+    w[3], w[H - 1] = float("inf"), float("-inf")
+    x[1, 3] = 0
+    y = cdl.rms_norm(x, w)
+    want = x.double() / torch.sqrt(x.double().pow(2).mean(-1, keepdim=True) + 1e-6) * w.double()
+    keep = torch.arange(H, device=DEV)
+    keep = (keep != 3) & (keep != H - 1)
+    a, b = y[:, ~keep].double(), want[:, ~keep]              # (infinite, or NaN where the element is zero)
+    assert bool(((a == b) | (a.isnan() & b.isnan())).all()) and bool(torch.isnan(y[1, 3])) and bool(torch.isinf(y[0, 3]))
+    ref, err = R.norm(x.double(), torch.where(keep, w, 0).double(), 1e-6)
+    R.assert_within(y[:, keep], ref[:, keep], R.to_bf16_bound(ref, err)[:, keep])
+    # h w = 2^140, h w r = 2^80
+    x, w = rand(g, T, H) * 2.0 ** 60, rand(g, H) * 2.0 ** 80
+    ref, err = R.norm(x.double(), w.double(), 1e-6)
+    assert bool(torch.isinf((x.float() * w.float())).any())
+    R.assert_within(cdl.rms_norm(x, w), ref, R.to_bf16_bound(ref, err))
+
+
+@pytest.mark.parametrize("flags", [0, 1])
+def test_quantised_infinite_values_are_the_dispatchs(flags):
+    """A value that an infinite weight makes infinite is quantised as the dispatch quantises an infinite element."""
+    announce("fp8 norm with infinite weights, flags %d" % flags)
+    g, T, H = gen(flags), 4, 384
+    x, w = rand(g, T, H), rand(g, H)
+    w[200] = float("inf")
+    y = torch.empty(T, H, dtype=BF, device=DEV)
+    q, s = cdl.rms_norm_fp8(x, w, scale_flags=flags, out=y)
+    assert bool(torch.isinf(y[:, 200]).all())
+    ids = torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+    dq, ds = cdl.dispatch_fp8(y, cdl.dispatch_layout(ids, 0, 1), rows=T, scale_flags=flags)
+    assert torch.equal(s[:, 1], ds[:, 1]) and torch.equal(q[:, 128:256], dq[:, 128:256])
