@@ -1076,6 +1076,14 @@ def _apart(t: Optional[torch.Tensor], name: str, same: Tuple[str, ...] = (), **o
                 raise ValueError("%s overlaps %s" % (name, other))
 
 
+def _outputs_apart(outs: dict, **operands) -> None:
+    """Given outputs share no memory with the operands or with each other."""
+    left = dict(outs)
+    for name, t in outs.items():
+        del left[name]
+        _apart(t, name, **operands, **left)
+
+
 def _groups(rows: torch.Tensor, name: str, L: int, counts, seg_indptr, status):
     """Checked rows of the grouped products, [rows, n] with seg_indptr and
     [L, cap, n] without: (number of rows, cap)."""
@@ -1121,8 +1129,8 @@ def _bf16_product(what, x, w, counts, seg_indptr, out, status, width_of, extra=N
     if extra is not None:
         _have(extra, "dh", torch.bfloat16, (*x.shape[:-1], n), x.device)
         more = (_ptr(extra),)
-    if out is not None:
-        _apart(out, "out", x=x, w=w, dh=extra)
+    if out is not None or status is not None:
+        _outputs_apart(dict(out=out, status=status), x=x, w=w, dh=extra, counts=counts, seg_indptr=seg_indptr)
     out = _product_rows(out, "out", x, width)
     _same_device(x.device, w=w)
     _launch(what, x.device, _ptr(x), rows, K, _ptr(w), L, n, *more, _ptr(counts), _ptr(seg_indptr), cap, _ptr(out),
@@ -1177,8 +1185,8 @@ def grouped_bf16_dx(dy: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg
     if dy.dim() < 2 or dy.shape[-1] != N:
         raise ValueError("dy must have rows of N = %d elements, got %s" % (N, tuple(dy.shape)))
     rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
-    if out is not None:
-        _apart(out, "out", dy=dy, w=w)
+    if out is not None or status is not None:
+        _outputs_apart(dict(out=out, status=status), dy=dy, w=w, counts=counts, seg_indptr=seg_indptr)
     out = _product_rows(out, "out", dy, K)
     _same_device(dy.device, w=w)
     _launch("cdl_grouped_bf16_dx", dy.device, _ptr(dy), rows, N, _ptr(w), L, K, _ptr(counts), _ptr(seg_indptr), cap,
@@ -1202,7 +1210,7 @@ def grouped_bf16_dw(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, seg
         out = torch.empty(L, N, K, dtype=torch.bfloat16, device=dy.device)
     else:
         _have(out, "out", torch.bfloat16, (L, N, K), dy.device)
-        _apart(out, "out", dy=dy, x=x)
+    _outputs_apart(dict(out=out, status=status), dy=dy, x=x, counts=counts, seg_indptr=seg_indptr)
     _same_device(dy.device, x=x)
     _launch("cdl_grouped_bf16_dw", dy.device, _ptr(dy), _ptr(x), rows, N, K, L, _ptr(counts), _ptr(seg_indptr), cap,
             _ptr(out), _ptr(status))
@@ -1234,8 +1242,9 @@ def grouped_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor, w_scal
     scale_flags format), w_q [L, N, K] and w_scales [L, ceil(N / 128), K / 128]
     as quant_fp8_blocks does.  Rows and counts as for grouped_bf16."""
     L, N, K, rows, cap = _fp8_args(q, scales, w_q, w_scales, counts, seg_indptr, scale_flags, status)
-    if out is not None:
-        _apart(out, "out", q=q, scales=scales, w_q=w_q, w_scales=w_scales)
+    if out is not None or status is not None:
+        _outputs_apart(dict(out=out, status=status), q=q, scales=scales, w_q=w_q, w_scales=w_scales, counts=counts,
+                       seg_indptr=seg_indptr)
     out = _product_rows(out, "out", q, N)
     _launch("cdl_grouped_fp8", q.device, _ptr(q), _ptr(scales), int(scale_flags), rows, K, _ptr(w_q), _ptr(w_scales), L, N,
             _ptr(counts), _ptr(seg_indptr), cap, _ptr(out), _ptr(status))
@@ -1254,8 +1263,8 @@ def grouped_swiglu_fp8(q: torch.Tensor, scales: torch.Tensor, w_q: torch.Tensor,
     I = _halves(N)
     if I % FP8_GROUP:
         raise CdlError(-3, "grouped_swiglu_fp8 (I must be a multiple of %d)" % FP8_GROUP)
-    _apart(out_q, "out_q", q=q, scales=scales, w_q=w_q, w_scales=w_scales, out_scales=out_scales)
-    _apart(out_scales, "out_scales", q=q, scales=scales, w_q=w_q, w_scales=w_scales)
+    _outputs_apart(dict(out_q=out_q, out_scales=out_scales, status=status), q=q, scales=scales, w_q=w_q, w_scales=w_scales,
+                   counts=counts, seg_indptr=seg_indptr)
     if out_q is None:
         out_q = torch.empty(*q.shape[:-1], I, dtype=torch.uint8, device=q.device)
     _need(out_q, "out_q", torch.uint8, (*q.shape[:-1], I))
