@@ -38,6 +38,11 @@ behind the norm that makes the rows:
     dgu = grouped_swiglu_bf16_grad(rows, w13, da, lay.counts, lay.seg_indptr)
     drows = grouped_bf16_dx(dgu, w13, lay.counts, lay.seg_indptr)
     dw13 = grouped_bf16_dw(dgu, rows, lay.counts, lay.seg_indptr)
+
+No call records anything for autograd.  The bf16 products, the norm and their
+gradients refuse tensors that require a gradient while one would be recorded:
+they are called under torch.no_grad(), or in the forward and backward of a
+torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -1076,6 +1081,15 @@ def _apart(t: Optional[torch.Tensor], name: str, same: Tuple[str, ...] = (), **o
                 raise ValueError("%s overlaps %s" % (name, other))
 
 
+def _no_autograd(**tensors) -> None:
+    """A result without the gradient that its caller waits for is no answer."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError("%s requires a gradient, which this call does not record: call it under torch.no_grad(), "
+                                 "or in a torch.autograd.Function" % name)
+
+
 def _outputs_apart(outs: dict, **operands) -> None:
     """Given outputs share no memory with the operands or with each other."""
     left = dict(outs)
@@ -1124,6 +1138,7 @@ def _bf16_product(what, x, w, counts, seg_indptr, out, status, width_of, extra=N
     if x.dim() < 2 or x.shape[-1] != K:
         raise ValueError("x must have rows of K = %d elements, got %s" % (K, tuple(x.shape)))
     rows, cap = _groups(x, "x", L, counts, seg_indptr, status)
+    _no_autograd(x=x, w=w, dh=extra, out=out)
     n, width = width_of(N)
     more = ()
     if extra is not None:
@@ -1185,6 +1200,7 @@ def grouped_bf16_dx(dy: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg
     if dy.dim() < 2 or dy.shape[-1] != N:
         raise ValueError("dy must have rows of N = %d elements, got %s" % (N, tuple(dy.shape)))
     rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
+    _no_autograd(dy=dy, w=w, out=out)
     if out is not None or status is not None:
         _outputs_apart(dict(out=out, status=status), dy=dy, w=w, counts=counts, seg_indptr=seg_indptr)
     out = _product_rows(out, "out", dy, K)
@@ -1205,6 +1221,7 @@ def grouped_bf16_dw(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor, seg
         raise ValueError("dy and x must have the same rows, got %s and %s" % (tuple(dy.shape), tuple(x.shape)))
     L = counts.numel()
     rows, cap = _groups(dy, "dy", L, counts, seg_indptr, status)
+    _no_autograd(dy=dy, x=x, out=out)
     N, K = dy.shape[-1], x.shape[-1]
     if out is None:
         out = torch.empty(L, N, K, dtype=torch.bfloat16, device=dy.device)
@@ -1382,6 +1399,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     normed); then returns (out, h), otherwise out.  out and residual_out may be
     x or residual itself."""
     T, H = _norm_args(x, weight, eps)
+    _no_autograd(x=x, weight=weight, residual=residual, out=out, residual_out=residual_out)
     residual_out = _norm_residual(x, weight, residual, out, residual_out)
     out = _same_rows(out, "out", x)
     _launch("cdl_rms_norm", x.device, _ptr(x), _ptr(residual), _ptr(weight), float(eps), T, H, _ptr(out),
@@ -1397,6 +1415,7 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     scale_flags).  Returns (q [T, H] uint8, scales) and with residual also h;
     `out`, where given, receives the bf16 rows as well (a router's input)."""
     T, H = _norm_args(x, weight, eps)
+    _no_autograd(x=x, weight=weight, residual=residual, out=out, residual_out=residual_out)
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
     if H % FP8_GROUP:
@@ -1439,6 +1458,7 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
     may be dy, h or dresidual itself.  Deterministic."""
     T, H = _norm_args(h, weight, eps)
     _have(dy, "dy", torch.bfloat16, h.shape, h.device)
+    _no_autograd(dy=dy, h=h, weight=weight, dresidual=dresidual, out=out, dweight=dweight)
     if dresidual is not None:
         _have(dresidual, "dresidual", torch.bfloat16, h.shape, h.device)
     if out is not None or dweight is not None or workspace is not None:

@@ -1,4 +1,4 @@
-"""What the binding of the bf16 and fp8 products refuses before any call of the
+"""What the binding of the bf16 and fp8 products and of the norm refuses before any call of the
 library (CPU only: the check for GPU tensors is left out, and a call that gets
 through is a failure)."""
 import math
@@ -82,3 +82,46 @@ def test_outputs_over_counts_segments_or_status(host, name):
     both = arena.cut(0, torch.int32, L)
     with pytest.raises(ValueError, match="status overlaps counts"):
         call(both, seg, both[1:])
+
+
+def differentiable():
+    """name, call(*operands), shapes of the operands"""
+    c, g = torch.zeros(L, dtype=torch.int32), torch.zeros(L + 1, dtype=torch.int64)
+    x, w, dy, dh, row = (T, K), (L, N, K), (T, N), (T, N // 2), (K,)
+    return [
+        ("grouped_bf16", lambda x, w: cdl.grouped_bf16(x, w, c, g), (x, w)),
+        ("grouped_swiglu_bf16", lambda x, w: cdl.grouped_swiglu_bf16(x, w, c, g), (x, w)),
+        ("grouped_swiglu_bf16_grad", lambda x, w, dh: cdl.grouped_swiglu_bf16_grad(x, w, dh, c, g), (x, w, dh)),
+        ("grouped_bf16_dx", lambda dy, w: cdl.grouped_bf16_dx(dy, w, c, g), (dy, w)),
+        ("grouped_bf16_dw", lambda dy, x: cdl.grouped_bf16_dw(dy, x, c, g), (dy, x)),
+        ("rms_norm", cdl.rms_norm, (x, row, x)),
+        ("rms_norm_fp8", cdl.rms_norm_fp8, (x, row, x)),
+        ("rms_norm_grad", lambda dy, h, w, d: cdl.rms_norm_grad(dy, h, w, 1e-6, d), (x, x, row, x)),
+    ]
+
+
+@pytest.mark.parametrize("name,call,shapes", differentiable())
+def test_tensors_that_require_a_gradient(host, name, call, shapes):
+    """They would get a result without one, silently."""
+    for which in range(len(shapes)):
+        args = [torch.zeros(s, dtype=BF) for s in shapes]
+        with pytest.raises(Launched, match=name):
+            call(*args)
+        args[which].requires_grad_()
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call(*args)
+        with torch.no_grad(), pytest.raises(Launched, match=name):
+            call(*args)
+
+        class Inside(torch.autograd.Function):               # no gradient is recorded within
+            @staticmethod
+            def forward(ctx, *a):
+                return call(*a)
+
+        with pytest.raises(Launched, match=name):
+            Inside.apply(*args)
+
+
+def test_weights_that_require_a_gradient_can_be_quantised(host):
+    with pytest.raises(Launched):
+        cdl.quant_fp8_blocks(torch.zeros(L, N, K, dtype=BF, requires_grad=True))
