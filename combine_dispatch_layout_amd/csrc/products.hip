@@ -894,6 +894,7 @@ struct ProductWg {
     __device__ __forceinline__ void store_tile_fp8(Work<(M > 0 ? M : 1)> &k)
     {
         constexpr int H = NF / 2;
+        static_assert(H == 4, "a lane's 16 codes are one store");
         float *amax = reinterpret_cast<float *>(lds + S::kAmax);
         if constexpr (M > 0) {
 #pragma unroll
@@ -942,17 +943,11 @@ struct ProductWg {
             }
             uint8_t *to = a.hq + row * I + at.n0 + wn * H * 16;
             const int g = lane >> 4;
-            if constexpr (H == 4) {
-                swap_halves(w[0], w[2]);
-                swap_halves(w[1], w[3]);
-                swap_rows16(w[0], w[1]);
-                swap_rows16(w[2], w[3]);
-                if (live) *reinterpret_cast<u32x4 *>(to + 16 * g) = u32x4{w[0], w[1], w[2], w[3]};
-            } else {
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-                    if (live) *reinterpret_cast<uint32_t *>(to + 16 * j + 4 * g) = w[j];
-            }
+            swap_halves(w[0], w[2]);
+            swap_halves(w[1], w[3]);
+            swap_rows16(w[0], w[1]);
+            swap_rows16(w[2], w[3]);
+            if (live) *reinterpret_cast<u32x4 *>(to + 16 * g) = u32x4{w[0], w[1], w[2], w[3]};
             if (live && lane < 16 && wn == 0) {
                 const int64_t grp = at.n0 / 128;
                 const int64_t r = a.h_mat ? at.e * a.h_mat + (at.m0 + t) * a.h_row : row * a.h_row;
