@@ -214,8 +214,13 @@ struct ProductShape {
     static constexpr size_t kLds = kAmax + (FP8 ? WN * MT * 4 : 0);   // then the tile table
 };
 
-// 1 / (1 + exp(-x)).  The reciprocal is within 1 ulp (the division costs ten
-// instructions, which a tile's epilogue pays up to 128 times a lane).
+// 1 / (1 + exp(-x)).  The exponential is the instruction's, whose argument x
+// log2(e) is rounded once (a relative error of |x| 2^-24 where the gate is far
+// below zero, else less), the reciprocal within 1 ulp: both far below the
+// rounding of the results.  A tile's epilogue takes them up to 128 times a lane:
+// 30000 rows of 40 experts, K = 320, N = 2112, bf16 SwiGLU 65 us, 76 with the
+// library's exponential and 88 with a division too (4096 rows, K = 7168: 350, 354,
+// 354).
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // What one side of a tile loads in a stage.
