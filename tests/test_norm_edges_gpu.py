@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import combine_dispatch_layout_amd as cdl
+import differences as D
 import products_ref as R
 from gpu_util import DEV, announce
 from test_products_gpu import BF, gen, rand
@@ -78,3 +79,15 @@ def test_quantised_infinite_values_are_the_dispatchs(flags):
     ids = torch.zeros(T, 1, dtype=torch.int32, device=DEV)
     dq, ds = cdl.dispatch_fp8(y, cdl.dispatch_layout(ids, 0, 1), rows=T, scale_flags=flags)
     assert torch.equal(s[:, 1], ds[:, 1]) and torch.equal(q[:, 128:256], dq[:, 128:256])
+
+
+@pytest.mark.parametrize("T,H", [(6, 200), (40, 2049), (3, 8320), (600, 64)])
+def test_gradient_has_the_slopes_of_differences(T, H):
+    announce("norm gradient, differences, T=%d H=%d" % (T, H))
+    g = gen(T)
+    h, dy, w = rand(g, T, H), rand(g, T, H), rand(g, H, scale=0.3) + 1
+    args, loss = [h.double(), w.double()], D.norm_loss(dy.double(), 1e-6)
+    dx, dw = cdl.rms_norm_grad(dy, h, w)
+    _, _, _, err_w = R.norm_grad(dy.double(), h.double(), w.double(), 1e-6, None)
+    assert D.slopes_agree(dx, loss, args, 0, g, R.BF16 * float(dx.double().norm()))
+    assert D.slopes_agree(dw, loss, args, 1, g, float(err_w.norm()))

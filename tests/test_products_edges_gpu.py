@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import combine_dispatch_layout_amd as cdl
+import differences as D
 import products_ref as R
 import products_tiles as tiles
 from gpu_util import DEV, announce
@@ -240,3 +241,34 @@ def test_a_row_has_the_same_bits_in_every_tile():
         for n, o in got[1:]:
             assert all(torch.equal(a, b) for a, b in zip(flat(o, n0), flat(first, n0))), (name, n)
         assert all(torch.equal(a, b) for a, b in zip(flat(got[4][1], 1500), flat(got[2][1], 1500))), name
+
+
+def test_training_pass_has_the_slopes_of_differences():
+    """The experts' layer as a torch.autograd.Function: its gradients against differences of the layer in 64 bits."""
+    announce("bf16 training pass, differences")
+    g, T, H, I, E, k = gen(31), 120, 64, 72, 4, 2
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, -1).indices.to(torch.int32)
+    lay, rows = cdl.permute(rand(g, T, H), ids, 0, E)
+    at = (lay.counts, lay.seg_indptr)
+
+    class Experts(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w13, w2):
+            h = cdl.grouped_swiglu_bf16(x, w13, *at)
+            ctx.save_for_backward(x, w13, w2, h)
+            return cdl.grouped_bf16(h, w2, *at)
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, w13, w2, h = ctx.saved_tensors
+            dgu = cdl.grouped_swiglu_bf16_grad(x, w13, cdl.grouped_bf16_dx(dy, w2, *at), *at)
+            return cdl.grouped_bf16_dx(dgu, w13, *at), cdl.grouped_bf16_dw(dgu, x, *at), cdl.grouped_bf16_dw(dy, h, *at)
+
+    w13, w2 = rand(g, E, 2 * I, H, scale=H ** -0.5), rand(g, E, H, I, scale=I ** -0.5)
+    dy = rand(g, rows.shape[0], H)
+    leaves = [t.clone().requires_grad_() for t in (rows, w13, w2)]
+    Experts.apply(*leaves).backward(dy)
+    args, loss = [w13.double(), w2.double(), rows.double()], D.experts_loss(dy.double(), lay.seg_indptr.tolist(), I)
+    # h, dh and dgu are rounded to bf16 on the way, at most two of them in a row before the result itself
+    for got, which in ((leaves[1].grad, 0), (leaves[2].grad, 1), (leaves[0].grad, 2)):
+        assert D.slopes_agree(got, loss, args, which, g, 3 * R.BF16 * float(got.double().norm())), which
