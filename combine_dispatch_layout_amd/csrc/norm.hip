@@ -11,8 +11,10 @@ namespace {
 // A row is read once and stays in registers: a workgroup of 256 threads (one
 // wave for up to 1024 columns) holds up to 32 elements of it a thread, units of
 // 8 (16 bytes) or, where rows are not 16-byte aligned, of 1.  Longer rows are
-// read twice.  Bound by the rows' bytes: 4096 x 7168 with residual to fp8 38 us
-// (206 MB, 5.4 TB/s), 16384 x 4096 to bf16 83 us (537 MB, 6.4 TB/s).
+// read twice.  Bound by the rows' bytes: 4096 x 7168 with residual to fp8 39 to
+// 41 us (206 MB, 5.1 TB/s), with the bf16 rows as well 45 (264 MB, 5.9), 16384 x
+// 4096 to bf16 83 to 94 us (537 MB, 5.7 to 6.4 TB/s).  Rows of units of 1 take
+// about three times as long: 4096 x 7167 122 us against 37.
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 constexpr int kNormHeld = 32 * kNormThreads;     // columns of a row held in registers
@@ -318,7 +320,10 @@ __global__ __launch_bounds__(kNormThreads) void rms_norm_long_kernel(NormArgs a)
 // A workgroup takes every G-th row and keeps its threads' columns of dweight in
 // registers; the G partial sums go to the workspace and a second kernel adds
 // them in order.  The next row's loads are under way while a row is summed.
-// 16384 x 4096 with residual: 110 us (537 MB, 4.9 TB/s), the sums 5 us.
+// 16384 x 4096 with residual: 103 to 112 us (537 MB, 4.8 to 5.2 TB/s), the sums 5
+// us of them.  Units of 1: 4096 x 7167 184 us against 44.  A narrow row still
+// takes a workgroup, two barriers and most of its threads idle: 16384 x 512 45 us
+// (1.5 TB/s), 200000 x 64 470 us (0.2 TB/s).
 // ---------------------------------------------------------------------------
 struct NormGradArgs {
     const uint16_t *dy, *h, *w, *dres;
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(1024) void rms_norm_dweight_kernel(const float *__r
 // ---------------------------------------------------------------------------
 
 // One block of 128 x 128 weights per workgroup: 16 lanes take a row's 128, a
-// thread 8 rows.
+// thread 8 rows.  32 x 4096 x 7168: 516 us (2.8 GB, 5.5 TB/s).
 __global__ __launch_bounds__(256) void quant_fp8_blocks_kernel(const uint16_t *__restrict__ w, int64_t N, int64_t K, int64_t NB,
                                                                int64_t G, int64_t blocks, uint8_t *__restrict__ q,
                                                                float *__restrict__ s)

@@ -27,11 +27,11 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 //
 // Measured, one MI355X: 128 tokens over 32 of 256 experts, K = 7168, N = 4096,
 // 306 us in bf16 and 160 in fp8 (6.0 and 5.8 TB/s); 131072 rows of 128 uneven
-// experts, K = N = 4096, 3.9 to 4.2 ms and 2.45 to 2.6 ms (1.1 and 1.75 PFLOP/s;
-// a library product of one such bf16 matrix 1.47), the matrix unit 66 and 48%
-// busy at 1.65 and 1.9 GHz.  In bf16 a tile of 64 stages loses about 9.5 us to
-// its end there, 3.6 of them to its output's bytes; with every tile loading the
-// same lines, which stay in the L2, it takes 3.4 ms.
+// experts, K = N = 4096, 3.8 to 4.2 ms and 2.4 to 2.6 ms (1.1 and 1.75 PFLOP/s; a
+// library product of one such matrix 1.47 to 1.58 and 3.0), the matrix unit 66 and
+// 48% busy at 1.65 and 1.9 GHz.  In bf16 it multiplies 12% more rows there than
+// exist; of 3.87 ms, 3.70 are left without its stores, and 3.41 with every tile
+// loading the same lines, which stay in the L2.
 // ---------------------------------------------------------------------------
 // The scale and codes of a group of 128 values in fp8 from its largest
 // magnitude (over its values that are not NaN; infinite if one is): the
@@ -1066,7 +1066,10 @@ bool product_fits(int32_t L)
 // one of 4096 rows: 138 / 159 / 112; 8 of 250 rows, K = N = 1024: 21 / 26 / 30.
 // Padded buffers are mostly empty in decode, where the weights' bytes count
 // and three stages of them in LDS pay: 4 rows an expert, 32 experts, K = 7168,
-// N = 4096, bf16 307 / 307 / 328, fp8 162 / 161 / 175.
+// N = 4096, bf16 307 / 307 / 328, fp8 162 / 161 / 175.  A full one loses by it:
+// 32 experts of 512 rows, K = N = 4096, bf16, 540 us at 192 rows, as segments (256)
+// 455.  A buffer of eight times the rows (the average is then no expert's) does not:
+// 4096 rows of 32 experts, K = 7168, SwiGLU, 361 us at 256 rows and 360 at 192.
 template <bool FP8, ProductForm FORM, ProductEpilogue EPI>
 int product_tile_rows(const ProductArgs &a)
 {
