@@ -666,6 +666,7 @@ int cdl_rms_norm(const uint16_t *x, const uint16_t *residual, const uint16_t *we
     int rc = check_norm(T, H, eps);
     if (rc != CDL_OK) return rc;
     if (T == 0) return CDL_OK;
+    if (!residual) residual_out = nullptr;                   // (ignored, its alignment too)
     if (!x || !weight || !out || (residual && !residual_out)) return CDL_ERR_NULL_POINTER;
     if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(out, 2) || !aligned(residual_out, 2))
         return CDL_ERR_UNSUPPORTED;
@@ -681,6 +682,7 @@ int cdl_rms_norm_fp8(const uint16_t *x, const uint16_t *residual, const uint16_t
     if (rc != CDL_OK) return rc;
     if (H % CDL_FP8_GROUP != 0 || !valid_scale_flags(scale_flags)) return CDL_ERR_UNSUPPORTED;
     if (T == 0) return CDL_OK;
+    if (!residual) residual_out = nullptr;
     if (!x || !weight || !out_q || !out_scales || (residual && !residual_out)) return CDL_ERR_NULL_POINTER;
     if (!vector_rows(H, {x, residual, weight, out, residual_out}) || !aligned(out_q, 8) || !aligned(out_scales, 4))
         return CDL_ERR_UNSUPPORTED;

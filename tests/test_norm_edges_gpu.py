@@ -91,3 +91,20 @@ def test_gradient_has_the_slopes_of_differences(T, H):
     _, _, _, err_w = R.norm_grad(dy.double(), h.double(), w.double(), 1e-6, None)
     assert D.slopes_agree(dx, loss, args, 0, g, R.BF16 * float(dx.double().norm()))
     assert D.slopes_agree(dw, loss, args, 1, g, float(err_w.norm()))
+
+
+def test_residual_out_without_residual_is_ignored():
+    """Whatever it is: it neither refuses the call nor takes it off the vector path, nor is written."""
+    announce("norm, C entry points, residual_out without residual")
+    g, T, H = gen(9), 5, 256
+    x, w = rand(g, T, H), rand(g, H)
+    want, (wq, ws) = cdl.rms_norm(x, w), cdl.rms_norm_fp8(x, w)
+    rest = torch.full((T * H + 8,), 0x55, dtype=torch.uint8, device=DEV)
+    y, q, s = torch.empty_like(want), torch.empty_like(wq), torch.empty_like(ws)
+    stream = torch.cuda.current_stream().cuda_stream
+    for off in (0, 1, 2):
+        ro = rest.data_ptr() + off
+        assert cdl.library().cdl_rms_norm(x.data_ptr(), None, w.data_ptr(), 1e-6, T, H, y.data_ptr(), ro, stream) == 0
+        assert cdl.library().cdl_rms_norm_fp8(x.data_ptr(), None, w.data_ptr(), 1e-6, T, H, q.data_ptr(), s.data_ptr(), 0, None,
+                                              ro, stream) == 0
+        assert torch.equal(y, want) and torch.equal(q, wq) and torch.equal(s, ws) and bool((rest == 0x55).all())
