@@ -1165,7 +1165,8 @@ def grouped_bf16(x: torch.Tensor, w: torch.Tensor, counts: torch.Tensor, seg_ind
     accumulation.  With seg_indptr, x is [rows, K] and expert e owns the
     counts[e] rows from seg_indptr[e]; without, x is the padded [L, cap, K]
     buffer and counts its masked_m.  Rows of no expert are left as they were.
-    Returns out [rows, N] or [L, cap, N]."""
+    The experts' segments may not overlap, and counts and seg_indptr not change
+    while the call runs.  Returns out [rows, N] or [L, cap, N]."""
     return _bf16_product("cdl_grouped_bf16", x, w, counts, seg_indptr, out, status, lambda N: (N, N))
 
 
@@ -1455,7 +1456,8 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
     rms_norm returned) [..., H] give (dx [..., H] bf16, dweight [H] fp32).  dx is
     the gradient of h, so of x and of residual alike; dresidual, the gradient
     that reaches h past the norm, is added to it before the one rounding.  out
-    may be dy, h or dresidual itself.  Deterministic."""
+    may be dy, h or dresidual itself.  Deterministic.  Calls that overlap, two
+    replayed graphs among them, need a workspace each."""
     T, H = _norm_args(h, weight, eps)
     _have(dy, "dy", torch.bfloat16, h.shape, h.device)
     _no_autograd(dy=dy, h=h, weight=weight, dresidual=dresidual, out=out, dweight=dweight)
